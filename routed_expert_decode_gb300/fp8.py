@@ -1,0 +1,240 @@
+"""Python binding of the block-scaled fp8 operators (C ABI in ``include/moe_fp8.h``).
+
+Argument marshalling only, as ``moe``: every operator runs in the library's CUDA
+kernels on the caller's tensors and stream, and a bad argument raises
+``MoeError`` (or ``ValueError`` for a tensor of another device, type or shape)
+before anything is enqueued.
+
+Entry points mirror the C names: ``group_route``, ``quantize``, ``swiglu``,
+``product``, ``combine``.  A row tensor may have any row stride, its columns are
+consecutive.  ``Layer`` runs them together as one routed layer.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import moe
+from .moe import MoeError, _check, _stream, check_device_error  # noqa: F401
+
+BLOCK = 128
+SCORE_SIGMOID = moe.SCORE_SIGMOID
+SCORE_SQRT_SOFTPLUS = moe.SCORE_SQRT_SOFTPLUS
+SCORE_SOFTMAX = 2
+GROUP_MAX = 0
+GROUP_TOP2_SUM = 1
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+_vp = ctypes.c_void_p
+_sz = ctypes.c_size_t
+_u32 = ctypes.c_uint32
+_int = ctypes.c_int
+
+
+class MoeRouter(ctypes.Structure):
+    _fields_ = [(n, _u32) for n in ("n_expert", "top_k", "n_group", "topk_group", "score",
+                                    "group_score", "renorm")] + [("s", ctypes.c_float)]
+
+
+class Fp8Mat(ctypes.Structure):
+    _fields_ = [("q", _vp), ("scale", _vp)]
+
+
+class Fp8Rows(ctypes.Structure):
+    _fields_ = [("q", _vp), ("scale", _vp), ("n", _u32), ("rows", _u32), ("off", _vp),
+                ("perm", _vp), ("top_k", _u32)]
+
+
+_lib = None
+
+
+def lib():
+    """The library with this header's signatures (loaded once; raises if absent)."""
+    global _lib
+    if _lib is None:
+        L = moe.lib()
+        _pr, _pm, _px = (ctypes.POINTER(t) for t in (MoeRouter, Fp8Mat, Fp8Rows))
+        L.moe_group_route_workspace_size.restype = _sz
+        L.moe_group_route_workspace_size.argtypes = [_pr, _u32]
+        L.moe_group_route.restype = _int
+        L.moe_group_route.argtypes = [_pr, _vp, _int, _sz, _vp, _u32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                      _sz, _vp]
+        L.moe_fp8_quantize.restype = _int
+        L.moe_fp8_quantize.argtypes = [_vp, _int, _sz, _u32, _u32, _vp, _vp, _vp]
+        L.moe_fp8_workspace_size.restype = _sz
+        L.moe_fp8_workspace_size.argtypes = [_u32]
+        L.moe_fp8_product.restype = _int
+        L.moe_fp8_product.argtypes = [_pm, _u32, _u32, _u32, _px, _vp, _int, _sz, _vp, _sz, _vp]
+        L.moe_fp8_swiglu.restype = _int
+        L.moe_fp8_swiglu.argtypes = [_pm, _pm, _u32, _u32, _u32, _px, _vp, _vp, _vp, _sz, _vp]
+        L.moe_fp8_combine.restype = _int
+        L.moe_fp8_combine.argtypes = [_vp, _int, _sz, _u32, _vp, _vp, _u32, _u32, _u32, _vp, _sz,
+                                      _vp, _int, _sz, _vp]
+        _lib = L
+    return _lib
+
+
+def blocks(n: int) -> int:
+    """Blocks of 128 that n columns take."""
+    return -(-n // BLOCK)
+
+
+def _rows2d(t: torch.Tensor, name: str):
+    """(pointer, dtype code, row stride) of a 2-d CUDA tensor with consecutive columns."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dt = DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    shape, (ld, step) = t.shape, t.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have consecutive columns")
+    return t.data_ptr(), dt, ld if shape[0] > 1 else shape[1]
+
+
+def _plane(t: torch.Tensor, dtypes, shape, name: str) -> int:
+    """Pointer of a contiguous CUDA tensor of one of the dtypes and this shape."""
+    if not t.is_cuda or t.dtype not in dtypes or not t.is_contiguous() or t.shape != shape:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtypes[0]} and shape "
+                         f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_U8 = (torch.uint8,)
+
+
+def _ws(ws: torch.Tensor):
+    return _plane(ws, _U8, (ws.numel(),), "ws"), ws.numel()
+
+
+# ------------------------------------------------------------------ router
+def make_router(n_expert: int, top_k: int, n_group: int = 1, topk_group: int = 1,
+                score: int = SCORE_SIGMOID, group_score: int = GROUP_TOP2_SUM,
+                renorm: bool = True, s: float = 1.0) -> MoeRouter:
+    return MoeRouter(n_expert, top_k, n_group, topk_group, score, group_score, int(renorm),
+                     float(s))
+
+
+def group_route_workspace_size(router: MoeRouter, T: int) -> int:
+    return int(lib().moe_group_route_workspace_size(ctypes.byref(router), T))
+
+
+def group_route(router: MoeRouter, logits, bias: Optional[torch.Tensor], idx, w, off, perm, pos,
+                ws, stream=None) -> None:
+    """moe_group_route: picks and weights of ``logits`` [T, E] (float32, bfloat16 or
+    float16), and the stable row permutation by expert."""
+    T, E = logits.shape
+    k = router.top_k
+    if E != router.n_expert:
+        raise ValueError(f"logits must have {router.n_expert} columns, got {E}")
+    lp, dt, ld = _rows2d(logits, "logits")
+    wsp, wsn = _ws(ws)
+    st = lib().moe_group_route(
+        ctypes.byref(router), lp, dt, ld,
+        None if bias is None else _plane(bias, _F32, (E,), "bias"), T,
+        _plane(idx, _I32, (T, k), "idx"), _plane(w, _F32, (T, k), "w"),
+        _plane(off, _I32, (E + 1,), "off"), _plane(perm, _I32, (T * k,), "perm"),
+        _plane(pos, _I32, (T, k), "pos"), wsp, wsn, _stream(stream))
+    if st:
+        _check("moe_group_route", st)
+
+
+# ------------------------------------------------------------------ quantiser
+def quantize(x, q, scale, stream=None) -> None:
+    """moe_fp8_quantize: rows of ``x`` [T, d] to e4m3 codes ``q`` [T, d] and fp32
+    scales ``scale`` [T, ceil(d / 128)]."""
+    T, d = x.shape
+    xp, dt, ld = _rows2d(x, "x")
+    st = lib().moe_fp8_quantize(xp, dt, ld, T, d, _plane(q, _CODES, (T, d), "q"),
+                                _plane(scale, _F32, (T, blocks(d)), "scale"), _stream(stream))
+    if st:
+        _check("moe_fp8_quantize", st)
+
+
+# ------------------------------------------------------------------ products
+class Mat:
+    """Weights of E experts: codes ``q`` [E, N, K] (or [N, K]: one expert) and
+    scales ``scale`` [E, ceil(N / 128), ceil(K / 128)].  Holds the tensors."""
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor):
+        if q.dim() == 2:
+            q, scale = q[None], scale[None]
+        self.E, self.N, self.K = q.shape
+        self.q, self.scale = q, scale
+        self.c = Fp8Mat(_plane(q, _CODES, q.shape, "q"),
+                        _plane(scale, _F32, (self.E, blocks(self.N), blocks(self.K)), "scale"))
+        self.ref = ctypes.byref(self.c)
+
+
+def workspace_size(rows: int) -> int:
+    """Bytes of workspace that ``swiglu`` and ``product`` need for this many output rows."""
+    return int(lib().moe_fp8_workspace_size(rows))
+
+
+def _activation(w: Mat, xq, xs, rows: int, off, perm, top_k: int):
+    n = xq.shape[0]
+    return Fp8Rows(_plane(xq, _CODES, (n, w.K), "xq"),
+                   _plane(xs, _F32, (n, blocks(w.K)), "xs"), n, rows,
+                   None if off is None else _plane(off, _I32, (w.E + 1,), "off"),
+                   None if perm is None else _plane(perm, _I32, (rows,), "perm"), top_k)
+
+
+def product(w: Mat, xq, xs, out, ws, off=None, perm=None, top_k: int = 1, stream=None) -> None:
+    """moe_fp8_product: ``out`` [R, N] = the activation rows times their expert's
+    weights, transposed.  ``off`` [E + 1] gives each expert's rows (None: one
+    expert, all rows); ``perm`` [R] with ``top_k`` makes row r read activation row
+    perm[r] // top_k (None: row r)."""
+    R, N = out.shape
+    if N != w.N:
+        raise ValueError(f"out must have {w.N} columns, got {N}")
+    op, dt, ld = _rows2d(out, "out")
+    x = _activation(w, xq, xs, R, off, perm, top_k)
+    wsp, wsn = _ws(ws)
+    st = lib().moe_fp8_product(w.ref, w.E, N, w.K, ctypes.byref(x), op, dt, ld, wsp, wsn,
+                               _stream(stream))
+    if st:
+        _check("moe_fp8_product", st)
+
+
+def swiglu(gate: Mat, up: Mat, xq, xs, hq, hs, ws, off=None, perm=None, top_k: int = 1,
+           stream=None) -> None:
+    """moe_fp8_swiglu: ``hq`` [R, f], ``hs`` [R, ceil(f / 128)] = silu(x Wg) * (x Wu),
+    quantised; rows as in ``product``."""
+    R = hq.shape[0]
+    if (up.E, up.N, up.K) != (gate.E, gate.N, gate.K):
+        raise ValueError("gate and up must have the same shape")
+    x = _activation(gate, xq, xs, R, off, perm, top_k)
+    wsp, wsn = _ws(ws)
+    st = lib().moe_fp8_swiglu(gate.ref, up.ref, gate.E, gate.N, gate.K, ctypes.byref(x),
+                              _plane(hq, _CODES, (R, gate.N), "hq"),
+                              _plane(hs, _F32, (R, blocks(gate.N)), "hs"), wsp, wsn,
+                              _stream(stream))
+    if st:
+        _check("moe_fp8_swiglu", st)
+
+
+# ------------------------------------------------------------------ combine
+def combine(o, w, pos, y, shared=None, stream=None) -> None:
+    """moe_fp8_combine: ``y`` [T, d] = ``shared`` [T, d] + sum over slots j of
+    ``w`` [T, k] * ``o`` [R, d] at row ``pos`` [T, k]."""
+    T, d = y.shape
+    R, k = o.shape[0], pos.shape[1]
+    if o.shape[1] != d or (shared is not None and shared.shape != (T, d)):
+        raise ValueError(f"o and shared must have {d} columns, shared {T} rows")
+    op, dt, ldo = _rows2d(o, "o")
+    yp, ydt, ldy = _rows2d(y, "y")
+    sp, lds = None, 0
+    if shared is not None:
+        sp, sdt, lds = _rows2d(shared, "shared")
+        if sdt != dt:
+            raise ValueError("shared must have o's type")
+    st = lib().moe_fp8_combine(op, dt, ldo, R, _plane(w, _F32, (T, k), "w"),
+                               _plane(pos, _I32, (T, k), "pos"), T, k, d, sp, lds, yp, ydt, ldy,
+                               _stream(stream))
+    if st:
+        _check("moe_fp8_combine", st)
