@@ -51,7 +51,7 @@ moe_status check_product(const moe_fp8_mat *w0, const moe_fp8_mat *w1, bool two,
   // tiles are numbered in 31 bits (the smallest are 32 rows by 128 columns)
   if (((uint64_t)x->rows / 32 + E) * fp8_blocks(N) >= (1ull << 31)) return MOE_ERR_INVALID_ARG;
   if (x->rows == 0) return MOE_OK;
-  if (!x->q || !x->scale || !is_aligned(x->scale, 4)) return MOE_ERR_INVALID_ARG;
+  if (x->n == 0 || !x->q || !x->scale || !is_aligned(x->scale, 4)) return MOE_ERR_INVALID_ARG;
   if (!ws || !is_aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < fp8_gemm_ws(x->rows)) return MOE_ERR_WORKSPACE;
   return MOE_OK;

@@ -141,6 +141,14 @@ __device__ __forceinline__ void fp8_block_scale(float amax, float &scale, float 
 }
 
 // ---------------------------------------------------------------- launchers
+// CTAs of a kernel that runs one per SM
+inline int fp8_ctas() {
+  int dev = 0, n = kSmCount;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    n = kSmCount;
+  return n < (int)kFp8MaxCtas ? n : (int)kFp8MaxCtas;
+}
 cudaError_t launch_fp8_quantize(const void *x, int dt, size_t ld, uint32_t T, uint32_t d, void *q,
                                 float *scale, cudaStream_t stream);
 cudaError_t launch_fp8_combine(const void *o, int dt, size_t ldo, uint32_t R, const float *w,

@@ -2,7 +2,7 @@
 // 128 x 128 weights and per row and 128 activations, on CUDA cores: the kernel
 // for operands that tensor copies cannot take (a reduction length that is not a
 // multiple of 16, code planes that are not 16-byte aligned).
-#include "fp8_tiles.cuh"
+#include "fp8_tc.cuh"
 
 namespace moe {
 namespace {
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kCoreThreads) k_fp8_core(const Fp8Args a) {
 }
 
 template <bool SWIGLU>
-cudaError_t run_core(Fp8Args &a, int sms, cudaStream_t stream) {
+cudaError_t run_core(Fp8Args &a, cudaStream_t stream) {
   auto kern = k_fp8_core<SWIGLU>;
   a.n_tiles = fp8_blocks(a.N);
   const size_t smem = 4 * ((size_t)(kCoreM + (SWIGLU ? 2 : 1) * kCoreN) * (kCoreSlab + 1)) +
@@ -133,20 +133,16 @@ cudaError_t run_core(Fp8Args &a, int sms, cudaStream_t stream) {
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, 4 * sms, kCoreThreads, smem, stream, true, a);
+  return launch_k(kern, 4 * fp8_ctas(), kCoreThreads, smem, stream, true, a);
 }
 
 }  // namespace
 
 size_t fp8_gemm_ws(uint32_t rows) {
-  (void)rows;
-  return MOE_WS_FIXED_BYTES;
+  return MOE_WS_FIXED_BYTES + fp8_tc_ws(rows);
 }
 
 cudaError_t launch_fp8_gemm(const Fp8Call &c) {
-  int dev = 0, sms = kSmCount;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   Fp8Args a = {};
   a.E = c.E;
   a.N = c.N;
@@ -170,7 +166,9 @@ cudaError_t launch_fp8_gemm(const Fp8Call &c) {
   a.odt = c.odt;
   a.err = (uint32_t *)c.ws;
   a.sync = (uint32_t *)(c.ws + 256) + kFp8TileSync;
-  return c.swiglu ? run_core<true>(a, sms, c.stream) : run_core<false>(a, sms, c.stream);
+  a.part = (float *)(c.ws + MOE_WS_FIXED_BYTES);
+  if (fp8_tc_ok(a)) return launch_fp8_tc(a, c.swiglu, c.stream);
+  return c.swiglu ? run_core<true>(a, c.stream) : run_core<false>(a, c.stream);
 }
 
 }  // namespace moe

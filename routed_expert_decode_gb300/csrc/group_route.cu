@@ -358,13 +358,6 @@ __global__ void __launch_bounds__(kGrThreads, 1) k_group_route(const GrArgs a) {
   }
 }
 
-int sm_count_here() {
-  int dev = 0, n = kSmCount;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : kSmCount;
-}
-
 // tokens per CTA and CTAs of a call
 void gr_split(uint32_t T, uint32_t sms, uint32_t *per, uint32_t *grid) {
   if (T <= kGrSoloTokens) {
@@ -424,8 +417,7 @@ cudaError_t launch_group_route(const moe_router &r, const void *logits, int dt, 
   a.sync = (uint32_t *)((uint8_t *)ws + 256) + kFp8RouteSync;
   a.err = (uint32_t *)ws;
   uint32_t grid;
-  const int sms = sm_count_here();
-  gr_split(T, sms < (int)kFp8MaxCtas ? (uint32_t)sms : kFp8MaxCtas, &a.per_cta, &grid);
+  gr_split(T, (uint32_t)fp8_ctas(), &a.per_cta, &grid);
   const uint32_t nper = (r.n_expert + 31) / 32;
   if (nper <= 1) return run_route<1>(a, grid, stream);
   if (nper <= 2) return run_route<2>(a, grid, stream);
