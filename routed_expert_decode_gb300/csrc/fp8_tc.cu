@@ -1,31 +1,40 @@
 // fp8_tc.cu -- routed and dense products over block-scaled e4m3 operands on the
 // 5th-generation tensor cores.
 //
-// A tile is up to MT activation rows of one expert by 256 weight rows (256
-// columns of the product; SwiGLU: the gate and up rows of one block of 128
-// features).  Per block of 128 along K, tcgen05.mma kind::f8f6f4 (M = 128, N =
-// 256, K = 32 four times) forms the unscaled products in one of two TMEM
+// A tile is a run of activation rows of one expert by NH blocks of 128 weight rows
+// (NH = 2: 256 columns of the product, or the gate and up rows of one block of 128
+// features).  Per block of 128 along K, tcgen05.mma kind::f8f6f4 (M = 128 rows a
+// CTA, K = 32 four times) forms the unscaled products in one of two TMEM
 // accumulators, and the epilogue warps add them, times scale_x * scale_w, to fp32
 // sums in registers: the scales change every 128 K, so each accumulator is read
 // once per block.  The activation rows sit on the MMA's M side, so that an
 // epilogue thread owns one row: its scale product is one scalar per block and
 // matrix, a pair of columns costs one packed FMA, and a row's quantisation block
-// after SwiGLU is a maximum over the thread's own registers.
+// after SwiGLU is a maximum over two threads' registers.
 //
 // Dead rows (tiles of a few rows) cost MMA time but no bytes: at M = 128 the
 // tensor cores consume a block's 32 KB of weights in ~512 clocks, HBM delivers an
 // SM's share of them in ~1400, so one layout serves decode and prefill.
-// Activation rows come by TMA gather (4 rows a request, through perm), so no
-// permuted copy of the activations is written.
+// Routed activation rows are copied by 16-byte cp.async through perm into the
+// swizzled layout, so no permuted copy of the activations is written (TMA's
+// gather of 4 rows a request took ~78 clocks a request, 2500 a tile of 128 rows);
+// rows in order come by one TMA box.
 //
-// Warps: 0 weights producer, 1 TMEM owner and MMA issuer, 2 activation producer,
-// 3 idle, 4..11 epilogue (warp w reads TMEM lanes 32*(w%4).., columns by half).
+// Many rows (CG = 2): a pair of CTAs works on 256 rows with cta_group::2, each SM
+// holding its own 128 rows and one of the two weight blocks, so that an SM takes in
+// 32 KB a block instead of 48 (an SM's share of L2's bandwidth is ~64 bytes a
+// clock, 768 clocks for 48 KB, against the MMA's 512).
 //
-// Work is split evenly over one CTA per SM: whole tiles in rounds of one per CTA,
-// and the tiles of the last, partial round cut along K into equal shares (first in
-// every CTA's order).  The shares of a tile meet in the workspace: each CTA writes
-// its fp32 sums, the last one to arrive adds all of them in ascending K, so the
-// result does not depend on the order of arrival.
+// Warps: 0 weights producer, 1 TMEM owner and MMA issuer (in the pair's second
+// CTA: it passes on that its activations have landed), 2 and 3 activations, 4..11
+// epilogue (warp w reads TMEM lanes 32*(w%4).., columns by half).
+//
+// Work goes out over one CTA (pair) per SM (pair): whole tiles in rounds, and the
+// tiles of the last, partial round cut along K into equal shares where whole tiles
+// would leave too many SMs idle (first in every CTA's order).  The shares of a
+// tile meet in the workspace: each CTA writes its fp32 sums, the last one to
+// arrive adds all of them in ascending K, so the result does not depend on the
+// order of arrival.
 #include <cuda.h>
 #include <string.h>
 
@@ -36,16 +45,17 @@ namespace {
 
 constexpr int kTcThreads = 12 * 32;
 constexpr int kEpiWarp0 = 4;
+constexpr int kMaxStages = 12;
 constexpr uint32_t kWBytes = 128 * 128;  // one weight box: 128 rows of one K block
 constexpr int kMinShare = 4;             // K blocks a CTA takes of a split round, at least
 constexpr long long kWaitCycles = 4000000000ll;  // ~2 s
 constexpr int kSpin = 1 << 26;
 constexpr int kHintNs = 20000;  // try_wait suspend-time hint: waiting warps sleep, not spin
-// registers per thread after the split: 128 * 64 + 256 * 216 <= 384 * 168
-constexpr int kRegsRole = 64, kRegsEpi = 216;
+// registers per thread after the split: 128 * 56 + 256 * 224 = 384 * 168, the launch's
+constexpr int kRegsRole = 56, kRegsEpi = 224;
 
 struct Fp8Maps {
-  CUtensorMap x;     // [n_x][K] codes, one row of 128 a box (gathered 4 at a time)
+  CUtensorMap x;     // [n_x][K] codes, box 128 x MT (rows in order)
   CUtensorMap w[2];  // [E][N][K] codes, box 128 x 128
 };
 
@@ -63,37 +73,88 @@ __device__ __forceinline__ void bar_expect(uint64_t *b, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(s32(b)), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity) {
+__device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(s32(b)), "r"(parity), "n"(kHintNs)
+      : "memory");
+  return done != 0;
+}
+// bounded by a clock budget and a count
+__device__ __forceinline__ bool bar_wait_long(uint64_t *b, uint32_t parity) {
   const long long t0 = clock64();
   for (int i = 0; i < kSpin; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(s32(b)), "r"(parity), "n"(kHintNs)
-        : "memory");
-    if (done) return true;
+    if (bar_try(b, parity)) return true;
     if (clock64() - t0 > kWaitCycles) return false;
   }
   return false;
 }
-__device__ __forceinline__ void tma_w(void *dst, const CUtensorMap *map, int k, int n, int e,
-                                      uint64_t *bar) {
+__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity) {
+  return bar_try(b, parity) || bar_wait_long(b, parity);
+}
+// arrive on the same barrier of the pair's first CTA
+__device__ __forceinline__ void bar_arrive_first(uint64_t *b) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(s32(dst)),
-      "l"(map), "r"(k), "r"(n), "r"(e), "r"(s32(bar))
+      "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, 0;\n"
+      " mbarrier.arrive.shared::cluster.b64 _, [r];\n}\n" ::"r"(s32(b))
       : "memory");
 }
-// four rows of the map's 128-byte boxes to consecutive rows of shared memory
-__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, int k,
-                                            const int (&row)[4], uint64_t *bar) {
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+}
+// Tensor copies.  In a pair (CG = 2) both CTAs' copies complete on the first CTA's
+// barrier: the address of a shared-memory object of this CTA with the bit that
+// tells the pair's CTAs apart cleared is the object's in the first.
+constexpr uint32_t kFirstCta = 0xFEFFFFFFu;
+template <int CG>
+__device__ __forceinline__ void tma_w(void *dst, const CUtensorMap *map, int k, int n, int e,
+                                      uint64_t *bar) {
+  if (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(s32(dst)),
+        "l"(map), "r"(k), "r"(n), "r"(e), "r"(s32(bar) & kFirstCta)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(s32(dst)),
+        "l"(map), "r"(k), "r"(n), "r"(e), "r"(s32(bar))
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void tma_x(void *dst, const CUtensorMap *map, int k, int row,
+                                      uint64_t *bar) {
+  if (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(s32(dst)),
+        "l"(map), "r"(k), "r"(row), "r"(s32(bar) & kFirstCta)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(s32(dst)),
+        "l"(map), "r"(k), "r"(row), "r"(s32(bar))
+        : "memory");
+}
+// 16 bytes global -> shared past L1, zeros beyond `bytes` of them; nothing unless go
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes, bool go) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(s32(dst)),
-      "l"(map), "r"(k), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(s32(bar))
+      "{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n"
+      " @p cp.async.cg.shared.global [%0], [%1], 16, %2;\n}\n" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"((int)go)
       : "memory");
+}
+// this thread arrives on b once its copies so far have landed
+__device__ __forceinline__ void cp_arrive(uint64_t *b) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(s32(b)) : "memory");
+}
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 __device__ __forceinline__ void tc_fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -102,20 +163,37 @@ __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 // called by a whole converged warp with uniform operands; one lane issues
+template <int CG>
 __device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                        uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n .reg .pred e, p;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
-      : "memory");
+  if (CG == 2)
+    asm volatile(
+        "{\n .reg .pred e, p;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred e, p;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
 }
+// arrive on b (in a pair: on both CTAs' b) when the MMAs so far are done
+template <int CG>
 __device__ __forceinline__ void tc_commit(uint64_t *bar) {
-  asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
-          s32(bar))
-      : "memory");
+  if (CG == 2)
+    asm volatile(
+        "{\n .reg .pred e;\n .reg .b16 m;\n elect.sync _|e, 0xffffffff;\n mov.b16 m, 3;\n"
+        " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+        ".multicast::cluster.b64 [%0], m;\n}\n" ::"r"(s32(bar))
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::
+            "r"(s32(bar))
+        : "memory");
 }
 // 32 consecutive fp32 columns of this warp's 32 TMEM lanes, no wait
 __device__ __forceinline__ void tc_ld32(uint32_t taddr, float (&v)[32]) {
@@ -130,12 +208,15 @@ __device__ __forceinline__ void tc_ld32(uint32_t taddr, float (&v)[32]) {
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-// waits for the warp's loads; v, the registers of the latest, pass through it so
-// that no use of them can move above the wait
+// waits for the warp's loads; the registers of v pass through it so that no use of
+// them can move above the wait (tie32: the same for a second load)
 __device__ __forceinline__ void tc_wait_ld32(float (&v)[32]) {
 #define R4(i) "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3])
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : R4(0), R4(4), R4(8), R4(12), R4(16), R4(20), R4(24), R4(28)::"memory");
+}
+__device__ __forceinline__ void tie32(float (&v)[32]) {
+  asm volatile("" : R4(0), R4(4), R4(8), R4(12), R4(16), R4(20), R4(24), R4(28));
 #undef R4
 }
 __device__ __forceinline__ void st_global32(void *p, const uint32_t (&v)[8]) {
@@ -149,27 +230,43 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
   return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-// instruction descriptor: D f32, A and B e4m3, both K-major, N >> 3 at bit 17, M = 128
+// instruction descriptor: D f32, A and B e4m3, both K-major, N >> 3 at bit 17, M >> 4
+// at bit 24 (M = 128 a CTA)
+template <int CG>
 __device__ __forceinline__ uint32_t idesc_for(uint32_t n) {
-  return (1u << 4) | ((n >> 3) << 17) | (8u << 24);
+  return (1u << 4) | ((n >> 3) << 17) | (8u * CG << 24);
 }
 
+// a place in a ring of n stages: its index and the parity of its current use
+struct Ring {
+  uint32_t i = 0, phase = 0;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++i == n) {
+      i = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 // ---------------------------------------------------------------- work split
-// A CTA's work in order: its share [pos, end) of the split tiles' K blocks, then
-// whole tiles split, split + G, ...  Every role walks the same list.
+// A worker (a CTA, or a pair) has in order: its share [pos, end) of the split
+// tiles' K blocks, then whole tiles split, split + G, ...  Every role walks the
+// same list.
 struct Seg {
   int tile, kb0, kb1;
 };
 struct Walk {
-  int n_all, split, share, kbs, grid;  // tiles, split tiles, K blocks per CTA, per tile
+  int n_all, share, kbs, grid;  // tiles, K blocks per worker of the split tiles, per tile
   int pos, end, next;
-  __device__ Walk(int n_all_, int kbs_) : n_all(n_all_), kbs(kbs_), grid(gridDim.x) {
-    split = n_all % grid;
+  // the last, partial round is split if it has fewer than split_below tiles
+  __device__ Walk(int n_all_, int kbs_, int worker, int workers, int split_below)
+      : n_all(n_all_), kbs(kbs_), grid(workers) {
+    const int rest = n_all % grid, split = rest < split_below ? rest : 0;
     const long long items = (long long)split * kbs;
     share = max((int)((items + grid - 1) / grid), min(kMinShare, kbs));
-    pos = (int)min(items, (long long)blockIdx.x * share);
+    pos = (int)min(items, (long long)worker * share);
     end = (int)min(items, (long long)pos + share);
-    next = split + blockIdx.x;
+    next = split + worker;
   }
   __device__ bool take(Seg &s) {
     if (pos < end) {
@@ -186,157 +283,218 @@ struct Walk {
     next += grid;
     return true;
   }
-  // CTAs that share split tile v
-  __device__ int first_cta(int v) const { return (int)((long long)v * kbs / share); }
-  __device__ int last_cta(int v) const { return (int)(((long long)(v + 1) * kbs - 1) / share); }
+  // workers that share split tile v
+  __device__ int first_worker(int v) const { return (int)((long long)v * kbs / share); }
+  __device__ int last_worker(int v) const { return (int)(((long long)(v + 1) * kbs - 1) / share); }
 };
 
-// Row r's product over one segment leaves 128 fp32 sums in each of its two
+// A row's product over one segment leaves up to 128 fp32 sums in each of its two
 // epilogue threads: acc[0..31] and acc[32..63] are pairs of columns -- of the
-// gate and the up block (SwiGLU), or of the two halves of 128 columns.
-template <bool SWIGLU, int MT>
+// gate and the up block (SwiGLU), or of a block's two halves.
+template <bool SWIGLU, int MT, int NH, int CG>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    k_fp8_tc(const Fp8Args a, const __grid_constant__ Fp8Maps maps, const int n_stages,
-             const bool vec) {
+    k_fp8_tc(const Fp8Args a, const __grid_constant__ Fp8Maps maps, const uint32_t n_stages,
+             const int split_below, const bool vec) {
+  static_assert((!SWIGLU || NH == 2) && (CG == 1 || (MT == 128 && NH == 2)), "tile shapes");
   pdl_trigger();
   extern __shared__ __align__(1024) uint8_t tsm_raw[];
   uint8_t *tsm = (uint8_t *)(((uintptr_t)tsm_raw + 1023) & ~(uintptr_t)1023);
-  constexpr uint32_t kABytes = MT * 128, kStage = kABytes + 2 * kWBytes;
+  constexpr int kRows = MT * CG;                 // rows of a tile
+  constexpr uint32_t kABytes = MT * 128;         // this CTA's activations of a stage
+  constexpr uint32_t kWStage = NH / CG * kWBytes;  // its weights
+  constexpr uint32_t kStage = kABytes + kWStage;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint8_t *ctrl = tsm + (size_t)n_stages * kStage;
-  uint64_t *full = (uint64_t *)ctrl;    // [8] operands of a stage landed
-  uint64_t *empty = full + 8;           // [8] ... consumed
-  uint64_t *d_full = empty + 8;         // [2] accumulator written
-  uint64_t *d_empty = d_full + 2;       // [2] ... read
-  uint64_t *pair = d_empty + 2;         // [4] the two epilogue warps of a lane quarter
+  const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0;  // CTA of the pair
+  uint8_t *ctrl = tsm + n_stages * kStage;
+  uint64_t *full = (uint64_t *)ctrl;     // [kMaxStages] operands of a stage landed
+  uint64_t *empty = full + kMaxStages;   // [kMaxStages] ... consumed
+  uint64_t *landed = empty + kMaxStages;  // [kMaxStages] second CTA: its activations landed
+  uint64_t *d_full = landed + kMaxStages;  // [2] accumulator written
+  uint64_t *d_empty = d_full + 2;        // [2] ... read
+  uint64_t *pair = d_empty + 2;          // [4] the two epilogue warps of a lane quarter
   uint32_t *tmem_holder = (uint32_t *)(pair + 4);
   volatile int *abort_flag = (volatile int *)(tmem_holder + 1);
   volatile int *last_part = (volatile int *)(tmem_holder + 2);  // [4]
-  float *ex = (float *)(ctrl + 256);                            // [2][2][128] row maxima
-  int *tiles_sm = (int *)(ctrl + 256 + 2048);
+  float *ex = (float *)(ctrl + 512);                            // [2][2][128] row maxima
+  int *tiles_sm = (int *)(ctrl + 512 + 2048);
+  const bool gather = a.perm != nullptr;
 
   if (tid == 0) {
-    for (int i = 0; i < 8; ++i) {
-      bar_init(&full[i], 2);
+    // arrivals on `full`: the weights' producer (with all bytes that tensor copies
+    // bring), and the 64 activation threads and the second CTA's forwarder (gather)
+    const uint32_t n_full = gather ? 1 + 64 + (CG - 1) : 1;
+    for (int i = 0; i < kMaxStages; ++i) {
+      bar_init(&full[i], n_full);
       bar_init(&empty[i], 1);
+      bar_init(&landed[i], 64);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&d_full[i], 1);
-      bar_init(&d_empty[i], 8);
+      bar_init(&d_empty[i], 8 * CG);
     }
     for (int i = 0; i < 4; ++i) bar_init(&pair[i], 2);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                     s32(tmem_holder))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if (CG == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                       s32(tmem_holder))
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                       s32(tmem_holder))
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (CG == 2) cluster_sync_all();  // both CTAs' barriers are set up
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   pdl_wait();
-  const RowTiles rt = fp8_row_tiles<MT>(a, tiles_sm);
-  Walk walk(rt.total * (int)a.n_tiles, (int)a.nbk);
+  const RowTiles rt = fp8_row_tiles<kRows>(a, tiles_sm);
+  const int worker = (int)blockIdx.x / CG;
+  Walk walk(rt.total * (int)a.n_tiles, (int)a.nbk, worker, (int)gridDim.x / CG, split_below);
   Seg seg;
   auto give_up = [&]() {
     atomicOr(a.err, kErrTimeout);
     *abort_flag = 1;
   };
-  // weight blocks of a tile: SwiGLU one of each matrix, else 2 (1 at the end of N)
-  auto halves = [&](const Fp8Tile &t) {
-    return SWIGLU || (uint32_t)t.nt * 256 + 128 < a.N ? 2 : 1;
+  // this CTA's share of a tile: rows from row0 on
+  auto my_tile = [&](int v) {
+    Fp8Tile t = fp8_tile<kRows>(a, rt, v);
+    t.row0 += MT * rank;
+    t.rows = max(0, min(MT, t.rows - MT * rank));
+    return t;
+  };
+  // weight blocks that a tile has: the last of an odd number stands alone
+  auto blocks_of = [&](const Fp8Tile &t) {
+    return SWIGLU ? 2 : min(NH, (int)a.nbn - t.nt * NH);
   };
 
   if (warp < kEpiWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRole));
     if (warp == 0 && lane == 0) {
-      // ============================ weights
-      uint32_t g = 0;
+      // ============================ weights (and activations in order)
+      Ring st;
       while (!*abort_flag && walk.take(seg)) {
-        const Fp8Tile t = fp8_tile<MT>(a, rt, seg.tile);
-        const int nh = halves(t);
-        for (int kb = seg.kb0; kb < seg.kb1; ++kb, ++g) {
-          const uint32_t s = g % n_stages;
-          if (g >= (uint32_t)n_stages && !bar_wait(&empty[s], (g / n_stages - 1) & 1)) {
+        const Fp8Tile t = my_tile(seg.tile);
+        const int nb = blocks_of(t);
+        // a pair's second weight block is the second CTA's; where it lies past N the
+        // copy brings zeros, and the pair always runs at the full width
+        const uint32_t bytes = CG == 2 ? CG * (kWBytes + (gather ? 0 : kABytes))
+                                       : nb * kWBytes + (gather ? 0 : kABytes);
+        for (int kb = seg.kb0; kb < seg.kb1; ++kb, st.next(n_stages)) {
+          const uint32_t s = st.i;
+          if (!bar_wait(&empty[s], st.phase ^ 1)) {  // the first use passes
             give_up();
             break;
           }
-          uint8_t *dst = tsm + (size_t)s * kStage + kABytes;
-          bar_expect(&full[s], nh * kWBytes);
+          uint8_t *buf = tsm + s * kStage, *dst = buf + kABytes;
+          if (rank == 0) bar_expect(&full[s], bytes);
+          if (!gather) tma_x<CG>(buf, &maps.x, kb * 128, t.row0, &full[s]);
           if (SWIGLU) {
-            tma_w(dst, &maps.w[0], kb * 128, t.nt * 128, t.e, &full[s]);
-            tma_w(dst + kWBytes, &maps.w[1], kb * 128, t.nt * 128, t.e, &full[s]);
+            if (CG == 2) {
+              tma_w<CG>(dst, &maps.w[rank], kb * 128, t.nt * 128, t.e, &full[s]);
+            } else {
+              tma_w<CG>(dst, &maps.w[0], kb * 128, t.nt * 128, t.e, &full[s]);
+              tma_w<CG>(dst + kWBytes, &maps.w[1], kb * 128, t.nt * 128, t.e, &full[s]);
+            }
+          } else if (CG == 2) {
+            tma_w<CG>(dst, &maps.w[0], kb * 128, (t.nt * 2 + rank) * 128, t.e, &full[s]);
           } else {
-            for (int h = 0; h < nh; ++h)
-              tma_w(dst + h * kWBytes, &maps.w[0], kb * 128, t.nt * 256 + 128 * h, t.e, &full[s]);
+            for (int h = 0; h < nb; ++h)
+              tma_w<CG>(dst + h * kWBytes, &maps.w[0], kb * 128, (t.nt * NH + h) * 128, t.e,
+                        &full[s]);
           }
         }
       }
       // the stages still in use: leave with no copy in flight
-      for (uint32_t i = g > (uint32_t)n_stages ? g - n_stages : 0; i < g; ++i)
-        if (!bar_wait(*abort_flag ? &full[i % n_stages] : &empty[i % n_stages],
-                      (i / n_stages) & 1))
+      for (uint32_t i = 0; i < n_stages; ++i, st.next(n_stages))
+        if (!bar_wait(*abort_flag && rank == 0 ? &full[st.i] : &empty[st.i], st.phase ^ 1))
           give_up();
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 0) {
       // ============================ MMA issuer
-      uint32_t g = 0;
+      Ring st, acc;
       while (!*abort_flag && walk.take(seg)) {
-        const Fp8Tile t = fp8_tile<MT>(a, rt, seg.tile);
-        const uint32_t idesc = idesc_for(128 * halves(t));
-        for (int kb = seg.kb0; kb < seg.kb1; ++kb, ++g) {
-          const uint32_t s = g % n_stages, b = g & 1;
-          if ((g >= 2 && !bar_wait(&d_empty[b], (g / 2 - 1) & 1)) ||
-              !bar_wait(&full[s], (g / n_stages) & 1)) {
+        const Fp8Tile t = my_tile(seg.tile);
+        const uint32_t idesc = idesc_for<CG>(CG == 2 ? 256 : 128 * blocks_of(t));
+        for (int kb = seg.kb0; kb < seg.kb1; ++kb, st.next(n_stages), acc.next(2)) {
+          const uint32_t s = st.i, b = acc.i;
+          if (!bar_wait(&full[s], st.phase) || !bar_wait(&d_empty[b], acc.phase ^ 1)) {
             give_up();
             break;
           }
+          // what cp.async wrote is read by the tensor core's proxy
+          if (gather) fence_async();
           tc_fence_after();
           __syncwarp();
-          const uint64_t ad = sw128_desc(s32(tsm + (size_t)s * kStage));
-          const uint64_t bd = sw128_desc(s32(tsm + (size_t)s * kStage + kABytes));
+          const uint64_t ad = sw128_desc(s32(tsm + s * kStage));
+          const uint64_t bd = sw128_desc(s32(tsm + s * kStage + kABytes));
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // 32 bytes along K: 2 in the descriptor's units
-            tc_mma(tmem + b * 256, ad + 2 * k, bd + 2 * k, idesc, k > 0);
-          tc_commit(&empty[s]);
-          tc_commit(&d_full[b]);
+            tc_mma<CG>(tmem + b * 256, ad + 2 * k, bd + 2 * k, idesc, k > 0);
+          tc_commit<CG>(&empty[s]);
+          tc_commit<CG>(&d_full[b]);
         }
       }
-    } else if (warp == 2) {
-      // ============================ activations: lane l gathers rows 4l..4l+3
-      uint32_t g = 0;
-      while (!*abort_flag && walk.take(seg)) {
-        const Fp8Tile t = fp8_tile<MT>(a, rt, seg.tile);
-        const int groups = (t.rows + 3) / 4;
-        int row[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // rows past the end repeat the last one; a bad one reads row 0 (flagged)
-          const int r = min(4 * lane + i, t.rows - 1);
-          row[i] = max(0, fp8_x_row(a, t.row0 + r));
-        }
-        for (int kb = seg.kb0; kb < seg.kb1; ++kb, ++g) {
-          const uint32_t s = g % n_stages;
-          if (g >= (uint32_t)n_stages && !bar_wait(&empty[s], (g / n_stages - 1) & 1)) {
+    } else if (warp == 1 && gather) {
+      // ============================ second CTA: its activations have landed
+      Ring st;
+      while (!*abort_flag && walk.take(seg))
+        for (int kb = seg.kb0; kb < seg.kb1; ++kb, st.next(n_stages)) {
+          if (!bar_wait(&landed[st.i], st.phase)) {
             give_up();
             break;
           }
-          if (lane == 0) bar_expect(&full[s], groups * 512);
-          __syncwarp();
-          if (lane < groups)
-            tma_gather4(tsm + (size_t)s * kStage + lane * 512, &maps.x, kb * 128, row, &full[s]);
+          fence_async();
+          if (lane == 0) bar_arrive_first(&full[st.i]);
+        }
+    } else if (warp >= 2 && gather) {
+      // ============================ activations through perm: in instruction j of
+      // MT / 8, warp w copies rows 8j + 4w .. + 3, eight lanes a row of 128 codes
+      constexpr int kJ = MT / 8;
+      const int r0 = 4 * (warp - 2) + lane / 8, chunk = lane & 7;
+      uint64_t *done = rank == 0 ? full : landed;
+      Ring st;
+      while (!*abort_flag && walk.take(seg)) {
+        const Fp8Tile t = my_tile(seg.tile);
+        int row[kJ];  // a bad one (flagged) reads row 0
+#pragma unroll
+        for (int j = 0; j < kJ; ++j)
+          row[j] = 8 * j + r0 < t.rows ? max(0, fp8_x_row(a, t.row0 + 8 * j + r0)) : -1;
+        for (int kb = seg.kb0; kb < seg.kb1; ++kb, st.next(n_stages)) {
+          const uint32_t s = st.i;
+          if (!bar_wait(&empty[s], st.phase ^ 1)) {
+            give_up();
+            break;
+          }
+          const uint32_t k0 = kb * 128 + chunk * 16;
+          const uint8_t *src = a.xq + (k0 < a.K ? k0 : 0);
+          const int bytes = k0 < a.K ? 16 : 0;
+          // 128-byte swizzle: chunk c of row r at c ^ (r % 8)
+          const uint32_t dst = s32(tsm + s * kStage) + r0 * 128 + ((chunk ^ r0) << 4);
+#pragma unroll
+          for (int j = 0; j < kJ; ++j)
+            cp16(dst + j * 1024, src + (size_t)(uint32_t)row[j] * a.K, bytes, row[j] >= 0);
+          cp_arrive(&done[s]);
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
     // ============================ epilogue
     const int ew = warp - kEpiWarp0, half = ew >> 2, quarter = warp & 3;
-    const int m = quarter * 32 + lane;  // row of the tile, TMEM lane
-    const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
+    const int m = quarter * 32 + lane;  // row of this CTA's tile, TMEM lane
+    // this warp's columns: 64 of each block (SwiGLU, or one block), or one block
+    constexpr bool kSplitBlock = SWIGLU || NH == 1;
+    constexpr int kChunks = SWIGLU || NH == 2 ? 4 : 2;  // of 32 columns
+    const uint32_t col0 = (uint32_t)(quarter * 32) << 16 | (kSplitBlock ? 64 : 128) * half;
+    constexpr uint32_t kCol1 = SWIGLU ? 128 : 64;  // from chunk 0 to chunk 2
     uint32_t g = 0, npair = 0;  // accumulators, and meetings of the pair, so far
     auto meet = [&]() -> bool {
       __syncwarp();
@@ -345,77 +503,103 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!ok) give_up();
       return ok;
     };
+    auto release = [&](uint32_t b) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2 && rank == 1) bar_arrive_first(&d_empty[b]);
+        else bar_arrive(&d_empty[b]);
+      }
+    };
     uint32_t n_ex = 0;
     while (!*abort_flag && walk.take(seg)) {
-      const Fp8Tile t = fp8_tile<MT>(a, rt, seg.tile);
-      const bool warp_live = quarter * 32 < t.rows && (SWIGLU || half < halves(t));
+      const Fp8Tile t = my_tile(seg.tile);
+      const bool warp_live = quarter * 32 < t.rows && (kSplitBlock || half < blocks_of(t));
       const bool live = warp_live && m < t.rows;
-      const float *xs = a.xs, *wa = a.wsc[0], *wb = a.wsc[0];
-      if (warp_live) {
-        const int r = t.row0 + min(m, t.rows - 1);
-        xs = a.xs + (size_t)max(0, fp8_x_row(a, r)) * a.nbk;
-        const size_t blk = SWIGLU ? t.nt : 2 * t.nt + half;
-        wa = a.wsc[0] + ((size_t)t.e * a.nbn + blk) * a.nbk;
-        wb = SWIGLU ? a.wsc[1] + ((size_t)t.e * a.nbn + blk) * a.nbk : wa;
-      }
-      float2 acc[64];
+      float2 acc[16 * kChunks];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      float sx = 0.0f, sa = 0.0f, sb = 0.0f;
-      if (warp_live) sx = xs[seg.kb0], sa = wa[seg.kb0], sb = wb[seg.kb0];
+      for (int i = 0; i < 16 * kChunks; ++i) acc[i] = make_float2(0.0f, 0.0f);
       bool ok = true;
-      for (int kb = seg.kb0; kb < seg.kb1; ++kb, ++g) {
-        const uint32_t b = g & 1;
-        if (!bar_wait(&d_full[b], (g / 2) & 1)) {
-          give_up();
-          ok = false;
-          break;
+      if (!warp_live) {
+        for (int kb = seg.kb0; ok && kb < seg.kb1; ++kb, ++g) {
+          ok = bar_wait(&d_full[g & 1], (g / 2) & 1);
+          if (ok) release(g & 1);
         }
-        if (warp_live) {
+        if (!ok) give_up();
+      } else {
+        const int r = t.row0 + min(m, t.rows - 1);
+        const size_t blk = kSplitBlock ? t.nt : 2 * t.nt + half;
+        const float *xs = a.xs + (size_t)max(0, fp8_x_row(a, r)) * a.nbk;
+        const float *wa = a.wsc[0] + ((size_t)t.e * a.nbn + blk) * a.nbk;
+        const float *wb = SWIGLU ? a.wsc[1] + ((size_t)t.e * a.nbn + blk) * a.nbk : wa;
+        float sx = xs[seg.kb0], sa = wa[seg.kb0], sb = SWIGLU ? wb[seg.kb0] : 0.0f;
+        auto fma32 = [&](float (&v)[32], int c, float s) {
+          const float2 s2 = make_float2(s, s);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            acc[16 * c + i] = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), s2, acc[16 * c + i]);
+        };
+        // Two loads of 32 columns are in flight at a time (a wait covers all of a
+        // thread's loads), the next pair issued as registers come free -- across
+        // the blocks too, so that a load's latency lies under the FMAs before it.
+        float v0[32], v1[32];
+        ok = bar_wait(&d_full[g & 1], (g / 2) & 1);
+        if (ok) {
           tc_fence_after();
-          const float s0 = sx * sa, s1 = sx * sb;
-          // the next block's scales, on the way while this one is added
-          const int kn = min(kb + 1, seg.kb1 - 1);
-          sx = xs[kn], sa = wa[kn], sb = wb[kn];
-          const uint32_t base = lane_addr + b * 256;
-          const uint32_t c0 = SWIGLU ? 64 * half : 128 * half, c1 = SWIGLU ? 128 + 64 * half
-                                                                           : 128 * half + 64;
-          float v[2][32];
-          tc_ld32(base + c0, v[0]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tc_wait_ld32(v[c & 1]);
-            if (c < 3) tc_ld32(base + (c < 1 ? c0 + 32 : c1 + 32 * (c - 1)), v[(c + 1) & 1]);
-            const float s = c < 2 ? s0 : s1;
-            const float2 s2 = make_float2(s, s);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              acc[16 * c + i] = __ffma2_rn(make_float2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), s2,
-                                           acc[16 * c + i]);
-          }
-          tc_fence_before();
+          const uint32_t base = tmem + col0 + (g & 1) * 256;
+          tc_ld32(base, v0);
+          tc_ld32(base + 32, v1);
         }
-        __syncwarp();
-        if (lane == 0) bar_arrive(&d_empty[b]);
+        for (int kb = seg.kb0; ok && kb < seg.kb1; ++kb, ++g) {
+          const uint32_t base = tmem + col0 + (g & 1) * 256;
+          const float s0 = sx * sa, s1 = SWIGLU ? sx * sb : s0;
+          const int kn = min(kb + 1, seg.kb1 - 1);
+          // the next block's scales, on the way while this one is added
+          sx = xs[kn], sa = wa[kn];
+          if (SWIGLU) sb = wb[kn];
+          tc_wait_ld32(v0);
+          tie32(v1);
+          if (kChunks == 4) {
+            fma32(v0, 0, s0);
+            tc_ld32(base + kCol1, v0);
+            fma32(v1, 1, s0);
+            tc_ld32(base + kCol1 + 32, v1);
+            tc_wait_ld32(v0);
+            tie32(v1);
+          }
+          release(g & 1);
+          fma32(v0, kChunks - 2, s1);
+          const bool more = kb + 1 < seg.kb1;
+          const uint32_t next = tmem + col0 + ((g + 1) & 1) * 256;
+          if (more) {
+            ok = bar_wait(&d_full[(g + 1) & 1], ((g + 1) / 2) & 1);
+            tc_fence_after();
+            if (ok) tc_ld32(next, v0);
+          }
+          fma32(v1, kChunks - 1, s1);
+          if (more && ok) tc_ld32(next + 32, v1);
+        }
+        if (!ok) give_up();
       }
       if (!ok) break;
-      // ---- a share of a tile: the last of its CTAs adds up all shares
+      // ---- a share of a tile: the last of its workers adds up all shares
       if (seg.kb1 - seg.kb0 < (int)a.nbk) {
         if (quarter * 32 >= t.rows) continue;  // both warps of the pair
-        const int c0 = walk.first_cta(seg.tile), n = walk.last_cta(seg.tile) - c0 + 1;
-        // part of CTA c: its second slot if it starts the tile, its first otherwise
+        const int c0 = walk.first_worker(seg.tile);
+        const int n = walk.last_worker(seg.tile) - c0 + 1;
+        // part of worker c: its second slot if it starts the tile, its first otherwise
         auto part = [&](int c) {
-          return (float4 *)(a.part + (size_t)(2 * c + (c == c0)) * a.part_stride) +
+          return (float4 *)(a.part + (size_t)(2 * (c * CG + rank) + (c == c0)) * a.part_stride) +
                  (size_t)(quarter * 2 + half) * 1024 + lane;
         };
-        float4 *mine = part((int)blockIdx.x);
+        float4 *mine = part(worker);
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < 8 * kChunks; ++i)
           __stcg(mine + 32 * i,
                  make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y));
         __threadfence();
         if (!meet()) break;
-        uint32_t *count = a.sync + 4 * seg.tile + quarter;
+        uint32_t *count = a.sync + 4 * (seg.tile * CG + rank) + quarter;
         if (half == 0 && lane == 0) {
           __threadfence();
           const bool last = atomicAdd(count, 1u) == (uint32_t)n - 1;
@@ -426,11 +610,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!last_part[quarter]) continue;
         __threadfence();
 #pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
+        for (int i = 0; i < 16 * kChunks; ++i) acc[i] = make_float2(0.0f, 0.0f);
         for (int p = 0; p < n; ++p) {
           const float4 *src = part(c0 + p);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
+          for (int i = 0; i < 8 * kChunks; ++i) {
             const float4 v = __ldcg(src + 32 * i);
             acc[2 * i].x += v.x;
             acc[2 * i].y += v.y;
@@ -443,12 +627,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int r = t.row0 + m;
       if (!SWIGLU) {
         if (!live) continue;
-        const uint32_t n0 = (uint32_t)t.nt * 256 + 128 * half;
+        const uint32_t n0 = (uint32_t)t.nt * (128 * NH) + (NH == 2 ? 128 : 64) * half;
         if (vec) {
           if (a.odt == MOE_DT_F32) {
             float *dst = (float *)a.out + (size_t)r * a.ld + n0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < 4 * kChunks; ++i)
               if (n0 + 8 * i < a.N) {
                 const uint32_t w[8] = {
                     __float_as_uint(acc[4 * i].x),     __float_as_uint(acc[4 * i].y),
@@ -461,7 +645,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint16_t *dst = (uint16_t *)a.out + (size_t)r * a.ld + n0;
             const bool bf = a.odt == MOE_DT_BF16;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 2 * kChunks; ++i)
               if (n0 + 16 * i < a.N) {
                 uint32_t w[8];
 #pragma unroll
@@ -473,7 +657,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
+          for (int i = 0; i < 16 * kChunks; ++i) {
             if (n0 + 2 * i < a.N) fp8_store(a, r, n0 + 2 * i, acc[i].x);
             if (n0 + 2 * i + 1 < a.N) fp8_store(a, r, n0 + 2 * i + 1, acc[i].y);
           }
@@ -485,8 +669,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         float amax = 0.0f;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          acc[i].x = fp8_swiglu_value(acc[i].x, acc[32 + i].x);
-          acc[i].y = fp8_swiglu_value(acc[i].y, acc[32 + i].y);
+          acc[i].x = fp8_swiglu_value(acc[i].x, acc[(kChunks * 8 + i) % (16 * kChunks)].x);
+          acc[i].y = fp8_swiglu_value(acc[i].y, acc[(kChunks * 8 + i) % (16 * kChunks)].y);
           amax = fmaxf(amax, fmaxf(fabsf(acc[i].x), fabsf(acc[i].y)));
         }
         float *e = ex + (n_ex++ & 1) * 256;
@@ -522,9 +706,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (CG == 2) cluster_sync_all();  // no arrival of the other CTA's is still to come
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (CG == 2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
 
@@ -562,18 +750,47 @@ bool byte_map(CUtensorMap *m, const void *base, uint64_t K, uint64_t d1, uint64_
 
 constexpr size_t kSmemLimit = 232448;
 
-template <bool SWIGLU, int MT>
-cudaError_t run_tc(Fp8Args &a, const Fp8Maps &maps, int sms, bool vec, cudaStream_t stream) {
-  auto kern = k_fp8_tc<SWIGLU, MT>;
-  const size_t stage = MT * 128 + 2 * (size_t)kWBytes;
-  const size_t rest = 1024 + 256 + 2048 + fp8_tiles_smem(a.E);
+template <bool SWIGLU, int MT, int NH, int CG>
+cudaError_t run_tc(Fp8Args &a, cudaStream_t stream) {
+  const int sms = fp8_ctas() / CG * CG;
+  a.n_tiles = SWIGLU ? a.nbn : (a.nbn + NH - 1) / NH;
+  const uint32_t quarters = ((a.R < 128 ? a.R : 128) + 31) / 32;
+  a.part_stride = (size_t)quarters * 8192;
+  Fp8Maps maps;
+  memset(&maps, 0, sizeof maps);
+  if (!byte_map(&maps.x, a.xq, a.K, a.n_x, 1, 2, MT) ||
+      !byte_map(&maps.w[0], a.wq[0], a.K, a.N, a.E, 3, 128) ||
+      (SWIGLU && !byte_map(&maps.w[1], a.wq[1], a.K, a.N, a.E, 3, 128)))
+    return cudaErrorInvalidValue;
+  if (!SWIGLU) maps.w[1] = maps.w[0];
+  // 32-byte stores: whole groups of 32 bytes inside every row
+  const uint32_t group = 32 / (SWIGLU ? 1 : (uint32_t)dtype_size(a.odt));
+  const bool vec = ((uintptr_t)a.out & 31) == 0 && a.N % group == 0 && a.ld % group == 0;
+  auto kern = k_fp8_tc<SWIGLU, MT, NH, CG>;
+  const size_t stage = MT * 128 + NH / CG * (size_t)kWBytes;
+  const size_t rest = 1024 + 512 + 2048 + fp8_tiles_smem(a.E);
   int ns = (int)((kSmemLimit - rest) / stage);
-  if (ns > 8) ns = 8;
+  if (ns > kMaxStages) ns = kMaxStages;
   const size_t smem = rest + ns * stage;
+  const int workers = sms / CG;
+  const int split_below = MT == 32 ? workers / 2 : workers * 7 / 8;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, sms, kTcThreads, smem, stream, true, a, maps, ns, vec);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = sms;
+  cfg.blockDim = kTcThreads;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, maps, (uint32_t)ns, split_below, vec);
 }
 
 }  // namespace
@@ -590,25 +807,12 @@ size_t fp8_tc_ws(uint32_t rows) {
 }
 
 cudaError_t launch_fp8_tc(Fp8Args &a, bool swiglu, cudaStream_t stream) {
-  const int sms = fp8_ctas();
-  const uint32_t quarters = ((a.R < 128 ? a.R : 128) + 31) / 32;
-  a.part_stride = (size_t)quarters * 8192;
-  a.n_tiles = swiglu ? a.nbn : (a.nbn + 1) / 2;
-  Fp8Maps maps;
-  memset(&maps, 0, sizeof maps);
-  if (!byte_map(&maps.x, a.xq, a.K, a.n_x, 1, 2, 1) ||
-      !byte_map(&maps.w[0], a.wq[0], a.K, a.N, a.E, 3, 128) ||
-      (swiglu && !byte_map(&maps.w[1], a.wq[1], a.K, a.N, a.E, 3, 128)))
-    return cudaErrorInvalidValue;
-  if (!swiglu) maps.w[1] = maps.w[0];
-  // 32-byte stores: whole groups of 32 bytes inside every row
-  const uint32_t group = 32 / (swiglu ? 1 : (uint32_t)dtype_size(a.odt));
-  const bool vec = ((uintptr_t)a.out & 31) == 0 && a.N % group == 0 && a.ld % group == 0;
-  if (swiglu)
-    return a.R <= 32 * a.E ? run_tc<true, 32>(a, maps, sms, vec, stream)
-                           : run_tc<true, 128>(a, maps, sms, vec, stream);
-  return a.R <= 32 * a.E ? run_tc<false, 32>(a, maps, sms, vec, stream)
-                         : run_tc<false, 128>(a, maps, sms, vec, stream);
+  const uint64_t R = a.R, E = a.E;
+  if (R <= 32 * E)
+    return swiglu ? run_tc<true, 32, 2, 1>(a, stream) : run_tc<false, 32, 1, 1>(a, stream);
+  if (R <= 192 * E)
+    return swiglu ? run_tc<true, 128, 2, 1>(a, stream) : run_tc<false, 128, 2, 1>(a, stream);
+  return swiglu ? run_tc<true, 128, 2, 2>(a, stream) : run_tc<false, 128, 2, 2>(a, stream);
 }
 
 }  // namespace moe

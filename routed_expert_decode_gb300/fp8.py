@@ -17,7 +17,7 @@ from typing import Optional
 import torch
 
 from . import moe
-from .moe import MoeError, _check, _stream, check_device_error  # noqa: F401
+from .moe import MoeError, _check, check_device_error  # noqa: F401
 
 BLOCK = 128
 SCORE_SIGMOID = moe.SCORE_SIGMOID
@@ -81,6 +81,17 @@ def blocks(n: int) -> int:
     return -(-n // BLOCK)
 
 
+# the raw handle of a device's current stream, without a torch.cuda.Stream object
+# around it (2.9 us of a call's ~6 otherwise)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _stream(stream, t: torch.Tensor):
+    """Handle of ``stream``, or of the current stream of t's device."""
+    return _raw_stream(t.get_device()) if stream is None else moe._stream(stream)
+
+
 def _rows2d(t: torch.Tensor, name: str):
     """(pointer, dtype code, row stride) of a 2-d CUDA tensor with consecutive columns."""
     if not t.is_cuda:
@@ -139,7 +150,7 @@ def group_route(router: MoeRouter, logits, bias: Optional[torch.Tensor], idx, w,
         None if bias is None else _plane(bias, _F32, (E,), "bias"), T,
         _plane(idx, _I32, (T, k), "idx"), _plane(w, _F32, (T, k), "w"),
         _plane(off, _I32, (E + 1,), "off"), _plane(perm, _I32, (T * k,), "perm"),
-        _plane(pos, _I32, (T, k), "pos"), wsp, wsn, _stream(stream))
+        _plane(pos, _I32, (T, k), "pos"), wsp, wsn, _stream(stream, logits))
     if st:
         _check("moe_group_route", st)
 
@@ -151,7 +162,8 @@ def quantize(x, q, scale, stream=None) -> None:
     T, d = x.shape
     xp, dt, ld = _rows2d(x, "x")
     st = lib().moe_fp8_quantize(xp, dt, ld, T, d, _plane(q, _CODES, (T, d), "q"),
-                                _plane(scale, _F32, (T, blocks(d)), "scale"), _stream(stream))
+                                _plane(scale, _F32, (T, blocks(d)), "scale"),
+                                _stream(stream, x))
     if st:
         _check("moe_fp8_quantize", st)
 
@@ -196,7 +208,7 @@ def product(w: Mat, xq, xs, out, ws, off=None, perm=None, top_k: int = 1, stream
     x = _activation(w, xq, xs, R, off, perm, top_k)
     wsp, wsn = _ws(ws)
     st = lib().moe_fp8_product(w.ref, w.E, N, w.K, ctypes.byref(x), op, dt, ld, wsp, wsn,
-                               _stream(stream))
+                               _stream(stream, out))
     if st:
         _check("moe_fp8_product", st)
 
@@ -213,7 +225,7 @@ def swiglu(gate: Mat, up: Mat, xq, xs, hq, hs, ws, off=None, perm=None, top_k: i
     st = lib().moe_fp8_swiglu(gate.ref, up.ref, gate.E, gate.N, gate.K, ctypes.byref(x),
                               _plane(hq, _CODES, (R, gate.N), "hq"),
                               _plane(hs, _F32, (R, blocks(gate.N)), "hs"), wsp, wsn,
-                              _stream(stream))
+                              _stream(stream, hq))
     if st:
         _check("moe_fp8_swiglu", st)
 
@@ -235,6 +247,6 @@ def combine(o, w, pos, y, shared=None, stream=None) -> None:
             raise ValueError("shared must have o's type")
     st = lib().moe_fp8_combine(op, dt, ldo, R, _plane(w, _F32, (T, k), "w"),
                                _plane(pos, _I32, (T, k), "pos"), T, k, d, sp, lds, yp, ydt, ldy,
-                               _stream(stream))
+                               _stream(stream, y))
     if st:
         _check("moe_fp8_combine", st)
