@@ -94,7 +94,7 @@ moe_status moe_fp8_quantize(const void *x, moe_dtype dt, size_t ld, uint32_t T, 
   if (!rows_ok(x, dt, ld, T, d) || !q || !scale || !is_aligned(scale, 4))
     return MOE_ERR_INVALID_ARG;
   // one warp per 8 blocks: the grid's CTAs are numbered in 31 bits
-  if ((uint64_t)T * (fp8_blocks(d) / 8 + 1) >= (1ull << 33)) return MOE_ERR_INVALID_ARG;
+  if ((uint64_t)T * (fp8_blocks(d) / 8 + 1) >= (1ull << 32)) return MOE_ERR_INVALID_ARG;
   return status_of(launch_fp8_quantize(x, dt, ld, T, d, q, scale, (cudaStream_t)stream));
 }
 
@@ -156,7 +156,7 @@ moe_status moe_fp8_combine(const void *o, moe_dtype dt, size_t ldo, uint32_t R, 
   if (shared && !rows_ok(shared, dt, lds, T, d)) return MOE_ERR_INVALID_ARG;
   if (!rows_ok(y, ydt, ldy, T, d) || !w || !pos || !is_aligned(w, 4) || !is_aligned(pos, 4))
     return MOE_ERR_INVALID_ARG;
-  if ((uint64_t)T * ((d + 255) / 256) >= (1ull << 33)) return MOE_ERR_INVALID_ARG;
+  if ((uint64_t)T * ((d + 255) / 256) >= (1ull << 31)) return MOE_ERR_INVALID_ARG;
   return status_of(launch_fp8_combine(o, dt, ldo, R, w, pos, T, top_k, d, shared, lds, y, ydt, ldy,
                                       (cudaStream_t)stream));
 }

@@ -1,24 +1,27 @@
 // group_route.cu -- group-limited top-k routing and the stable permutation of
 // the (token, slot) rows by expert, in one kernel.
 //
-// Selection, one warp per token.  Lane l owns the NPER consecutive experts
+// Selection, one warp per token.  The token's logits go to shared memory, where one
+// rolled loop turns them into selection values c (the code runs from a cold
+// instruction cache once per call: unrolled over a lane's experts it took 4.3 us a
+// token, 2000 instructions).  Then lane l holds the NPER consecutive experts
 // [l*NPER, (l+1)*NPER), so "lowest index" is "lowest lane, then lowest register"
 // and a group of experts is a run of lanes: where the group size is NPER times a
 // power of two, a group's best two c meet by shuffles inside the run; other
-// sizes go through shared memory.  Scores become order-preserving unsigned keys;
-// a round of top-k is one redux.sync maximum, one ballot (the lowest lane that
-// holds it wins) and a rescan of the winner's registers.
+// sizes are scanned in shared memory.  Scores become order-preserving unsigned
+// keys; a round of top-k is one redux.sync maximum, one ballot (the lowest lane
+// that holds it wins) and a rescan of the winner's registers.
 //
 // Permutation.  A token picks an expert at most once, so the rank of row (t, j)
 // among its expert's rows of a run of tokens is a population count: bit t of the
 // expert's token mask is set, and the bits below t are the rows before it.  No
 // order of atomics enters the result.  Each CTA owns a contiguous run of
 // tokens, writes its count per expert, and after a grid-wide barrier adds up
-// the counts of the CTAs before it and of the experts before each expert.
+// the counts of the CTAs before it and of the experts before each expert.  A
+// call of a few rows counts them directly.
 //
-// What bounds it: about 500 warp instructions a token, so the issue slots for
-// many tokens (the logits are read once, 16 bytes a lane); for few tokens the
-// chain load -> score -> k rounds, which one CTA without the barrier runs.
+// What bounds it: the issue slots for many tokens (the logits are read once);
+// for few tokens the chain load -> score -> k rounds in one CTA.
 #include <float.h>
 
 #include "fp8_common.cuh"
@@ -31,6 +34,7 @@ constexpr int kGrThreads = kGrWarps * 32;
 constexpr uint32_t kGrMaskTokens = 128;  // tokens ranked at a time: 4 mask words per expert
 constexpr uint32_t kGrMaskWords = kGrMaskTokens / 32;
 constexpr uint32_t kGrSoloTokens = kGrWarps;  // up to one token a warp: one CTA, no barrier
+constexpr uint32_t kGrFewRows = 64;  // up to here, rows are ranked by comparing them all
 constexpr long long kGrWaitCycles = 4000000000ll;
 constexpr int kGrSpinIters = 1 << 26;
 
@@ -59,64 +63,88 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 __device__ __forceinline__ float no_nan(float v) { return v == v ? v : -INFINITY; }
 
+__device__ __forceinline__ float logit_value(float v) { return fminf(no_nan(v), FLT_MAX); }
 __device__ __forceinline__ float load_logit(const void *p, int dt, size_t i) {
   float v;
   if (dt == MOE_DT_F32) v = ((const float *)p)[i];
   else if (dt == MOE_DT_BF16) v = __bfloat162float(((const __nv_bfloat16 *)p)[i]);
   else v = __half2float(((const __half *)p)[i]);
-  return fminf(no_nan(v), FLT_MAX);
+  return logit_value(v);
+}
+// a token's E logits to shared memory by its warp
+template <int DT>
+__device__ __forceinline__ void stage_logits(const void *p, size_t row, uint32_t E, int lane,
+                                             float *sl) {
+  const typename Elem<DT>::T *src = (const typename Elem<DT>::T *)p + row;
+#pragma unroll 8
+  for (uint32_t i = lane; i < E; i += 32) sl[i] = logit_value(Elem<DT>::to(src[i]));
 }
 
 // sigmoid and sqrt(softplus) with CUDA's expf and log1pf; -inf gives 0
-__device__ __forceinline__ float score_of(float l, uint32_t fn) {
-  if (fn == MOE_SCORE_SQRT_SOFTPLUS)
-    return __fsqrt_rn(fmaxf(l, 0.0f) + log1pf(expf(-fabsf(l))));
-  return __fdiv_rn(1.0f, 1.0f + expf(-l));
+__device__ __forceinline__ float sigmoid_of(float l) { return __frcp_rn(1.0f + expf(-l)); }
+__device__ __forceinline__ float softplus_root_of(float l) {
+  return __fsqrt_rn(fmaxf(l, 0.0f) + log1pf(expf(-fabsf(l))));
 }
 // e^(l - max) of a row: 0 at -inf, a row of nothing else included
 __device__ __forceinline__ float softmax_term(float l, float m) {
   return l == -INFINITY ? 0.0f : expf(l - m);
 }
 
-// One token by one warp: its picks to idx/w and to s_pick (shared, [k]).
-// sc: E floats of shared memory of the warp (used for group sizes that are not
-// runs of whole lanes).
+// One token by one warp: its picks to idx/w and to s_pick (shared, [32]).
+// sc: 32 * NPER floats of shared memory of the warp.
 template <int NPER>
 __device__ __forceinline__ void route_token(const GrArgs &a, uint32_t t, int lane, int32_t *s_pick,
                                             float *sc) {
   const uint32_t E = a.r.n_expert, k = a.r.top_k, G = a.r.n_group;
   const uint32_t e0 = (uint32_t)lane * NPER;
   const size_t row = (size_t)t * a.ld;
-  const bool soft = a.r.score == MOE_SCORE_SOFTMAX;
-  float l[NPER], c[NPER];
-#pragma unroll
-  for (int i = 0; i < NPER; ++i)
-    l[i] = e0 + i < E ? load_logit(a.logits, a.dt, row + e0 + i) : -INFINITY;
+  const uint32_t fn = a.r.score;
+  __syncwarp();
+  if (a.dt == MOE_DT_F32) stage_logits<MOE_DT_F32>(a.logits, row, E, lane, sc);
+  else if (a.dt == MOE_DT_BF16) stage_logits<MOE_DT_BF16>(a.logits, row, E, lane, sc);
+  else stage_logits<MOE_DT_F16>(a.logits, row, E, lane, sc);
+  // each lane's own entries so far: no warp barrier needed until the runs are read
   float m = -INFINITY, rsum = 0.0f;  // softmax: the row's maximum and 1 / sum
-  if (soft) {
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) m = fmaxf(m, l[i]);
+  if (fn == MOE_SCORE_SOFTMAX) {
+#pragma unroll 1
+    for (uint32_t i = lane; i < E; i += 32) m = fmaxf(m, sc[i]);
     m = key_value(__reduce_max_sync(0xffffffffu, order_key(m)));
     float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) sum += softmax_term(l[i], m);
+#pragma unroll 1
+    for (uint32_t i = lane; i < E; i += 32) sum += softmax_term(sc[i], m);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     rsum = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
   }
-  const bool by_logit = soft && !a.bias && a.r.group_score == MOE_GROUP_MAX;
-  uint32_t key[NPER];
-#pragma unroll
-  for (int i = 0; i < NPER; ++i) {
-    if (e0 + i < E) {
-      c[i] = by_logit ? l[i] : soft ? softmax_term(l[i], m) * rsum : score_of(l[i], a.r.score);
-      if (a.bias) c[i] = no_nan(c[i] + a.bias[e0 + i]);
-      key[i] = order_key(c[i]);
-    } else {
-      c[i] = -INFINITY;
-      key[i] = 0u;  // below every expert
+  auto score = [&](float l) {
+    return fn == MOE_SCORE_SIGMOID ? sigmoid_of(l)
+           : fn == MOE_SCORE_SOFTMAX ? softmax_term(l, m) * rsum : softplus_root_of(l);
+  };
+  // selection values; by logit, they are what is staged
+  if (fn != MOE_SCORE_SOFTMAX || a.bias || a.r.group_score != MOE_GROUP_MAX) {
+#pragma unroll 1
+    for (uint32_t i = lane; i < E; i += 32) {
+      const float p = score(sc[i]);
+      sc[i] = a.bias ? no_nan(p + a.bias[i]) : p;
     }
   }
+  __syncwarp();
+  uint32_t key[NPER];
+  if (NPER % 4 == 0) {  // 16 bytes a load: free of bank conflicts
+#pragma unroll
+    for (int i = 0; i < NPER; i += 4) {
+      const float4 v = *(const float4 *)(sc + e0 + i);
+      key[i] = order_key(v.x);
+      key[(i + 1) % NPER] = order_key(v.y);
+      key[(i + 2) % NPER] = order_key(v.z);
+      key[(i + 3) % NPER] = order_key(v.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) key[i] = order_key(sc[e0 + i]);
+  }
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) key[i] = e0 + i < E ? key[i] : 0u;
   // ---- groups: drop the experts of those that are not kept
   if (a.r.topk_group < G) {
     const uint32_t gs = a.gsize;
@@ -124,81 +152,78 @@ __device__ __forceinline__ void route_token(const GrArgs &a, uint32_t t, int lan
     const uint32_t run = gs / NPER;
     float mine = -INFINITY;  // lane g: the score of group g
     if (gs % NPER == 0 && (run & (run - 1)) == 0) {
-      float b1 = -INFINITY, b2 = -INFINITY;
+      uint32_t b1 = 0u, b2 = 0u;  // the two best keys
 #pragma unroll
       for (int i = 0; i < NPER; ++i) {
-        b2 = fmaxf(b2, fminf(b1, c[i]));
-        b1 = fmaxf(b1, c[i]);
+        b2 = max(b2, min(b1, key[i]));
+        b1 = max(b1, key[i]);
       }
+#pragma unroll 1
       for (uint32_t o = 1; o < run; o <<= 1) {
-        const float p1 = __shfl_xor_sync(0xffffffffu, b1, o);
-        const float p2 = __shfl_xor_sync(0xffffffffu, b2, o);
-        b2 = fmaxf(fmaxf(b2, p2), fminf(b1, p1));
-        b1 = fmaxf(b1, p1);
+        const uint32_t p1 = __shfl_xor_sync(0xffffffffu, b1, o);
+        const uint32_t p2 = __shfl_xor_sync(0xffffffffu, b2, o);
+        b2 = max(max(b2, p2), min(b1, p1));
+        b1 = max(b1, p1);
       }
-      const float s = two ? no_nan(b1 + b2) : b1;
+      const float s = two ? no_nan(key_value(b1) + key_value(b2)) : key_value(b1);
       mine = __shfl_sync(0xffffffffu, s, min((uint32_t)lane * run, 31u));
-    } else {
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < NPER; ++i)
-        if (e0 + i < E) sc[e0 + i] = c[i];
-      __syncwarp();
-      if ((uint32_t)lane < G) {
-        float b1 = -INFINITY, b2 = -INFINITY;
-        for (uint32_t i = 0; i < gs; ++i) {
-          const float v = sc[lane * gs + i];
-          b2 = fmaxf(b2, fminf(b1, v));
-          b1 = fmaxf(b1, v);
-        }
-        mine = two ? no_nan(b1 + b2) : b1;
+    } else if ((uint32_t)lane < G) {
+      float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll 1
+      for (uint32_t i = 0; i < gs; ++i) {
+        const float v = sc[lane * gs + i];
+        b2 = fmaxf(b2, fminf(b1, v));
+        b1 = fmaxf(b1, v);
       }
-      __syncwarp();
+      mine = two ? no_nan(b1 + b2) : b1;
     }
+    __syncwarp();
     const uint32_t gk = (uint32_t)lane < G ? order_key(mine) : 0u;
     uint32_t before = 0;  // groups that go before this lane's
+#pragma unroll 1
     for (uint32_t g = 0; g < G; ++g) {
       const uint32_t ok = __shfl_sync(0xffffffffu, gk, g);
       before += ok > gk || (ok == gk && g < (uint32_t)lane);
     }
     const uint32_t kept =
         __ballot_sync(0xffffffffu, (uint32_t)lane < G && before < a.r.topk_group);
+    if (gs % NPER == 0) {  // a lane's experts are of one group
+      if (!((kept >> (e0 / gs)) & 1u)) {
 #pragma unroll
-    for (int i = 0; i < NPER; ++i)
-      if (e0 + i < E && !((kept >> ((e0 + i) / gs)) & 1u)) key[i] = 0u;
+        for (int i = 0; i < NPER; ++i) key[i] = 0u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NPER; ++i)
+        if (e0 + i < E && !((kept >> ((e0 + i) / gs)) & 1u)) key[i] = 0u;
+    }
   }
   // ---- top k
   uint32_t best = 0u;
 #pragma unroll
   for (int i = 0; i < NPER; ++i) best = max(best, key[i]);
   int mine = 0;  // lane j: the expert of slot j
+#pragma unroll 1
   for (uint32_t j = 0; j < k; ++j) {
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
     const int win = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
-    int e = 0;
+    int at = 0;  // the winner's first register that holds it
     if (lane == win) {
-      bool found = false;
+#pragma unroll
+      for (int i = NPER - 1; i >= 0; --i) at = key[i] == top ? i : at;
       best = 0u;
 #pragma unroll
       for (int i = 0; i < NPER; ++i) {
-        if (!found && key[i] == top) {
-          found = true;
-          e = (int)e0 + i;
-          key[i] = 0u;
-        }
+        key[i] = i == at ? 0u : key[i];
         best = max(best, key[i]);
       }
     }
-    e = __shfl_sync(0xffffffffu, e, win);
+    const int e = win * NPER + __shfl_sync(0xffffffffu, at, win);
     if ((uint32_t)lane == j) mine = e;
   }
   // ---- weights: lane j evaluates its pick's p again from the logit
   const bool pick = (uint32_t)lane < k;
-  float p = 0.0f;
-  if (pick) {
-    const float lj = load_logit(a.logits, a.dt, row + mine);
-    p = soft ? softmax_term(lj, m) * rsum : score_of(lj, a.r.score);
-  }
+  const float p = pick ? score(load_logit(a.logits, a.dt, row + mine)) : 0.0f;
   float w = a.r.s * p;
   if (a.r.renorm) {
     float sum = p;
@@ -209,7 +234,7 @@ __device__ __forceinline__ void route_token(const GrArgs &a, uint32_t t, int lan
   if (pick) {
     a.idx[(size_t)t * k + lane] = mine;
     a.w[(size_t)t * k + lane] = w;
-    if (s_pick) s_pick[lane] = mine;
+    s_pick[lane] = mine;
   }
 }
 
@@ -244,27 +269,50 @@ __device__ bool grid_barrier(uint32_t *sync, uint32_t n, uint32_t *err) {
 }
 
 template <int NPER>
-__global__ void __launch_bounds__(kGrThreads, 1) k_group_route(const GrArgs a) {
+__global__ void __launch_bounds__(kGrThreads, 1) k_group_route(const GrArgs a, const bool few) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ __align__(16) uint8_t gsm[];
   const uint32_t E = a.r.n_expert, k = a.r.top_k;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t *mask = (uint32_t *)gsm;                  // [E][kGrMaskWords]
-  int32_t *cnt = (int32_t *)(mask + E * kGrMaskWords);  // [E]: rows, then next row per expert
-  int32_t *scan = cnt + E;                           // [32]
-  int32_t *s_pick = scan + 32;                       // [kGrWarps][k]: solo call's picks
-  float *sc = (float *)(s_pick + kGrWarps * 32);     // [kGrWarps][E] or nothing
-  float *my_sc = sc + (size_t)warp * E;
+  float *sc = (float *)gsm + warp * (32 * NPER);  // a warp's staged logits
+  int32_t *s_pick = (int32_t *)gsm + blockDim.x * NPER;  // [kGrWarps][32]: latest picks
+  uint32_t *mask = (uint32_t *)(s_pick + kGrWarps * 32);  // [E][kGrMaskWords]
+  int32_t *cnt = (int32_t *)(mask + E * kGrMaskWords);    // [E]: rows, then next row per expert
+  int32_t *scan = cnt + E;                        // [32]
   const bool solo = gridDim.x == 1;
   const uint32_t t0 = min(a.T, blockIdx.x * a.per_cta), t1 = min(a.T, t0 + a.per_cta);
+  const uint32_t n_warps = blockDim.x / 32;
 
+  if (few) {
+    if ((uint32_t)warp < a.T) route_token<NPER>(a, warp, lane, s_pick + warp * 32, sc);
+    __syncthreads();
+    const uint32_t R = a.T * k;
+    for (uint32_t e = tid; e <= E; e += blockDim.x) {
+      int n = 0;
+      for (uint32_t t = 0; t < a.T; ++t)
+        for (uint32_t j = 0; j < k; ++j) n += s_pick[t * 32 + j] < (int)e;
+      a.off[e] = n;
+    }
+    for (uint32_t r = tid; r < R; r += blockDim.x) {
+      const uint32_t tr = r / k;
+      const int e = s_pick[tr * 32 + r - tr * k];
+      int rank = 0;
+      for (uint32_t t = 0; t < a.T; ++t)
+        for (uint32_t j = 0; j < k; ++j) {
+          const int v = s_pick[t * 32 + j];
+          rank += v < e || (v == e && t < tr);
+        }
+      a.perm[rank] = (int32_t)r;
+      a.pos[r] = rank;
+    }
+    return;
+  }
   for (uint32_t i = tid; i < E; i += kGrThreads) cnt[i] = 0;
   __syncthreads();
-  for (uint32_t t = t0 + warp; t < t1; t += kGrWarps) {
-    route_token<NPER>(a, t, lane, s_pick + warp * 32, my_sc);
+  for (uint32_t t = t0 + warp; t < t1; t += n_warps) {
+    route_token<NPER>(a, t, lane, s_pick + warp * 32, sc);
     if ((uint32_t)lane < k) atomicAdd(&cnt[s_pick[warp * 32 + lane]], 1);
-    __syncwarp();
   }
   __syncthreads();
 
@@ -376,15 +424,18 @@ template <int NPER>
 cudaError_t run_route(const GrArgs &a, uint32_t grid, cudaStream_t stream) {
   auto kern = k_group_route<NPER>;
   const uint32_t E = a.r.n_expert;
-  const bool sc = a.r.topk_group < a.r.n_group;
-  const size_t smem =
-      4 * ((size_t)E * kGrMaskWords + E + 32 + kGrWarps * 32 + (sc ? (size_t)kGrWarps * E : 0));
+  const bool few = grid == 1 && a.T * a.r.top_k <= kGrFewRows;
+  // few rows: a warp a token, and enough of them to write off[]
+  const uint32_t threads = few ? 32 * (a.T > 8 ? a.T : 8) : kGrThreads;
+  const size_t smem = 4 * ((size_t)kGrWarps * 32 + threads * NPER +
+                           (few ? 0 : (size_t)E * (kGrMaskWords + 1) + 32));
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  if (grid == 1) return launch_k(kern, 1, kGrThreads, smem, stream, true, a);
+  if (grid == 1) return launch_k(kern, 1, threads, smem, stream, true, a, few);
   GrArgs args = a;
-  void *p[] = {&args};
+  bool no = false;
+  void *p[] = {&args, &no};
   return cudaLaunchCooperativeKernel((const void *)kern, dim3(grid), dim3(kGrThreads), p, smem,
                                      stream);
 }
