@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kCoreThreads) k_fp8_core(const Fp8Args a) {
 template <bool SWIGLU>
 cudaError_t run_core(Fp8Args &a, cudaStream_t stream) {
   auto kern = k_fp8_core<SWIGLU>;
-  a.n_tiles = fp8_blocks(a.N);
+  fp8_set_tiles(a, fp8_blocks(a.N));
   const size_t smem = 4 * ((size_t)(kCoreM + (SWIGLU ? 2 : 1) * kCoreN) * (kCoreSlab + 1)) +
                       fp8_tiles_smem(a.E);
   const cudaError_t e =
@@ -167,7 +167,9 @@ cudaError_t launch_fp8_gemm(const Fp8Call &c) {
   a.err = (uint32_t *)c.ws;
   a.sync = (uint32_t *)(c.ws + 256) + kFp8TileSync;
   a.part = (float *)(c.ws + MOE_WS_FIXED_BYTES);
-  if (fp8_tc_ok(a)) return launch_fp8_tc(a, c.swiglu, c.stream);
+  if (fp8_tc_ok(a))
+    return a.R <= kFp8FewRows * a.E ? launch_fp8_few(a, c.swiglu, c.stream)
+                                    : launch_fp8_tc(a, c.swiglu, c.stream);
   return c.swiglu ? run_core<true>(a, c.stream) : run_core<false>(a, c.stream);
 }
 

@@ -22,11 +22,27 @@ struct Fp8Args {
   size_t ld;
   float *hs;
   int odt;
-  uint32_t n_tiles;    // column tiles of an expert
+  uint32_t n_tiles, n_tiles_inv;  // column tiles of an expert, floor((2^32 - 1) / that)
   uint32_t *err, *sync;
   float *part;         // partial sums of split tiles
   size_t part_stride;  // floats per part
 };
+
+// Before the wait for the stream's earlier work: the arguments into the constant
+// cache (a launch's are always cold, and the first uses come one after another)
+// and the routing arrays' lines on their way to L2 (a prefetch there reads nothing).
+__device__ __forceinline__ void fp8_warm(const Fp8Args &a) {
+  asm volatile("" ::"r"(a.E), "r"(a.N), "r"(a.nbn), "r"(a.nbk), "r"(a.R), "r"(a.top_k), "l"(a.xq),
+               "l"(a.xs), "l"(a.off), "l"(a.perm), "l"(a.wsc[0]), "l"(a.wsc[1]), "l"(a.out),
+               "l"(a.hs), "r"(a.n_tiles), "r"(a.n_tiles_inv), "l"(a.err), "l"(a.sync),
+               "l"(a.part));
+  auto prefetch = [](const int32_t *p, uint32_t n) {
+    const uint32_t i = threadIdx.x * 32;
+    if (p && i < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
+  };
+  prefetch(a.off, a.E + 1);
+  prefetch(a.perm, a.R);
+}
 
 // activation row of output row r; -1 (flagged) if perm names none
 __device__ __forceinline__ int fp8_x_row(const Fp8Args &a, int r) {
@@ -43,48 +59,62 @@ struct RowTiles {
   int total;
 };
 
-// called by all threads (a multiple of 32, at most 1024); sm: 2(E+1) + 34 ints
+// called by all threads; sm: 2(E+1) + 1 ints.  One warp does it, a run of experts a
+// lane, behind a single block barrier: it is on every call's critical path.
 template <int MT>
 __device__ __forceinline__ RowTiles fp8_row_tiles(const Fp8Args &a, int *sm) {
-  int *s_off = sm, *s_tile = sm + (a.E + 1), *wsum = s_tile + (a.E + 1), *flag = wsum + 32;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x;
-  if (tid == 0) *flag = 0;
-  for (int e = tid; e <= (int)a.E; e += nthr)
-    s_off[e] = a.off ? a.off[e] : e == 0 ? 0 : (int)a.R;
-  __syncthreads();
-  const int per = ((int)a.E + nthr - 1) / nthr;
-  const int b = min((int)a.E, tid * per), e1 = min((int)a.E, b + per);
-  int sum = 0;
-  for (int e = b; e < e1; ++e) {
-    const int rows = s_off[e + 1] - s_off[e];
-    if (rows < 0 || s_off[e] < 0 || s_off[e + 1] > (int)a.R) *flag = 1;
-    sum += (max(rows, 0) + MT - 1) / MT;
-  }
-  int incl = sum;
+  int *s_off = sm, *s_tile = sm + (a.E + 1), *s_total = s_tile + (a.E + 1);
+  const int E = (int)a.E, R = (int)a.R;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const int per = (E + 31) / 32, b = min(E, lane * per), e1 = min(E, b + per);
+    auto off = [&](int e) { return a.off ? a.off[e] : e == 0 ? 0 : R; };
+    int at = off(b), tiles = 0;
+    bool bad = at < 0 || at > R;
+    if (per <= 8) {
+      int next[8];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+      for (int i = 0; i < 8; ++i) next[i] = b + i < e1 ? off(b + i + 1) : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (b + i < e1) {
+          s_off[b + i] = at;
+          s_tile[b + i] = tiles;  // within the lane's run so far
+          bad |= next[i] < at || next[i] > R;
+          tiles += (max(next[i] - at, 0) + MT - 1) / MT;
+          at = next[i];
+        }
+    } else {
+#pragma unroll 8
+      for (int e = b; e < e1; ++e) {
+        const int next = off(e + 1);
+        s_off[e] = at;
+        s_tile[e] = tiles;
+        bad |= next < at || next > R;
+        tiles += (max(next - at, 0) + MT - 1) / MT;
+        at = next;
+      }
+    }
+    int incl = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    for (int e = b; e < e1; ++e) s_tile[e] += incl - tiles;
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 31) {
+      s_off[E] = at;
+      s_tile[E] = incl;
+      *s_total = bad ? 0 : incl;
+      if (bad) atomicOr(a.err, kErrBadOffsets);
+    }
   }
-  if (lane == 31) wsum[warp] = incl;
-  __syncthreads();
-  int run = incl - sum, total = 0;
-  for (int w = 0; w < nthr / 32; ++w) {
-    if (w < warp) run += wsum[w];
-    total += wsum[w];
-  }
-  for (int e = b; e < e1; ++e) {
-    s_tile[e] = run;
-    run += (max(s_off[e + 1] - s_off[e], 0) + MT - 1) / MT;
-  }
-  if (tid == 0) s_tile[a.E] = total;
-  const bool bad = *flag != 0;
-  if (bad && tid == 0) atomicOr(a.err, kErrBadOffsets);
   __syncthreads();
   RowTiles t;
   t.off = s_off;
   t.tile = s_tile;
-  t.total = bad ? 0 : total;
+  t.total = *s_total;
   return t;
 }
 
@@ -96,8 +126,10 @@ struct Fp8Tile {
 // after another, its row tiles innermost (they share the weights)
 template <int MT>
 __device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Args &a, const RowTiles &rt, int v) {
-  // expert e's tiles are [tile[e] * n_tiles, tile[e+1] * n_tiles)
-  const int q = v / (int)a.n_tiles;
+  // expert e's tiles are [tile[e] * n_tiles, tile[e+1] * n_tiles); v / n_tiles by the
+  // host's reciprocal, whose quotient is at most one short
+  int q = (int)__umulhi((uint32_t)v, a.n_tiles_inv);
+  if (v - q * (int)a.n_tiles >= (int)a.n_tiles) ++q;
   int lo = 0, hi = (int)a.E;  // largest e with tile[e] <= q (experts without rows share a prefix)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -107,14 +139,19 @@ __device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Args &a, const RowTiles &rt
   const int local = v - rt.tile[lo] * (int)a.n_tiles;
   Fp8Tile t;
   t.e = lo;
-  t.nt = local / mt;
+  t.nt = mt == 1 ? local : local / mt;
   const int m = local - t.nt * mt;
   t.row0 = rt.off[lo] + m * MT;
   t.rows = min(MT, rt.off[lo + 1] - t.row0);
   return t;
 }
 
-inline size_t fp8_tiles_smem(uint32_t E) { return 4 * (2 * ((size_t)E + 1) + 34); }
+inline size_t fp8_tiles_smem(uint32_t E) { return 4 * (2 * ((size_t)E + 1) + 2); }
+
+inline void fp8_set_tiles(Fp8Args &a, uint32_t n_tiles) {
+  a.n_tiles = n_tiles;
+  a.n_tiles_inv = 0xffffffffu / n_tiles;
+}
 
 // store one output value of the product
 __device__ __forceinline__ void fp8_store(const Fp8Args &a, int r, uint32_t n, float v) {
