@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kCoreThreads) k_fp8_core(const Fp8Args a) {
 template <bool SWIGLU>
 cudaError_t run_core(Fp8Args &a, cudaStream_t stream) {
   auto kern = k_fp8_core<SWIGLU>;
-  fp8_set_tiles(a, fp8_blocks(a.N));
+  fp8_set_tiles(a, fp8_blocks(a.N), 1);
   const size_t smem = 4 * ((size_t)(kCoreM + (SWIGLU ? 2 : 1) * kCoreN) * (kCoreSlab + 1)) +
                       fp8_tiles_smem(a.E);
   const cudaError_t e =

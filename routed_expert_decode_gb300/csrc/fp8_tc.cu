@@ -72,7 +72,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t *d_full = landed + kMaxStages;  // [2] accumulator written
   uint64_t *d_empty = d_full + 2;        // [2] ... read
   uint64_t *pair = d_empty + 2;          // [4] the two epilogue warps of a lane quarter
-  uint32_t *tmem_holder = (uint32_t *)(pair + 4);
+  uint64_t *drain = pair + 4;            // the MMAs of an aborted call
+  uint32_t *tmem_holder = (uint32_t *)(drain + 1);
   volatile int *abort_flag = (volatile int *)(tmem_holder + 1);
   volatile int *last_part = (volatile int *)(tmem_holder + 2);  // [4]
   float *ex = (float *)(ctrl + 512);                            // [2][2][128] row maxima
@@ -98,6 +99,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bar_init(&d_empty[i], 8 * CG);
     }
     for (int i = 0; i < 4; ++i) bar_init(&pair[i], 2);
+    bar_init(drain, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -123,12 +125,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   pdl_wait();
   const RowTiles rt = fp8_row_tiles<kRows>(a, tiles_sm);
   const int worker = (int)blockIdx.x / CG;
-  Walk walk(rt.total * (int)a.n_tiles, (int)a.nbk, worker, (int)gridDim.x / CG, split_below);
+  Walk walk(rt.total * (int)a.n_tiles, a, worker, (int)gridDim.x / CG, split_below);
   Seg seg;
-  auto give_up = [&]() {
-    atomicOr(a.err, kErrTimeout);
-    *abort_flag = 1;
-  };
+  const Guard guard{a.err, abort_flag};
   // this CTA's share of a tile: rows from row0 on
   auto my_tile = [&](int v) {
     Fp8Tile t = fp8_tile<kRows>(a, rt, v);
@@ -143,10 +142,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp < kEpiWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRole));
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ============================ weights (and activations in order)
       Ring st;
-      while (!*abort_flag && walk.take(seg)) {
+      while (!guard.aborted() && walk.take(seg)) {
         const Fp8Tile t = my_tile(seg.tile);
         const int nb = blocks_of(t);
         // a pair's second weight block is the second CTA's; where it lies past N the
@@ -155,10 +154,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                        : nb * kWBytes + (gather ? 0 : kABytes);
         for (int kb = seg.kb0; kb < seg.kb1; ++kb, st.next(n_stages)) {
           const uint32_t s = st.i;
-          if (!bar_wait(&empty[s], st.phase ^ 1)) {  // the first use passes
-            give_up();
-            break;
-          }
+          bar_wait(&empty[s], st.phase ^ 1, guard);  // the first use passes
+          if (guard.aborted()) break;
+          if (lane) continue;
           uint8_t *buf = tsm + s * kStage, *dst = buf + kABytes;
           if (rank == 0) bar_expect(&full[s], bytes);
           if (!gather) tma_x<CG>(buf, &maps.x, kb * 128, t.row0, &full[s]);
@@ -180,24 +178,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       // the stages still in use: leave with no copy in flight
       for (uint32_t i = 0; i < n_stages; ++i, st.next(n_stages))
-        if (!bar_wait(*abort_flag && rank == 0 ? &full[st.i] : &empty[st.i], st.phase ^ 1))
-          give_up();
+        if (!bar_wait_for(*abort_flag && rank == 0 ? &full[st.i] : &empty[st.i], st.phase ^ 1))
+          atomicOr(a.err, kErrTimeout);
     } else if (warp == 1 && rank == 0) {
       // ============================ MMA issuer
       Ring st, acc;
-      while (!*abort_flag && walk.take(seg)) {
+      while (!guard.aborted() && walk.take(seg)) {
         const Fp8Tile t = my_tile(seg.tile);
         const uint32_t idesc = idesc_for<CG>(CG == 2 ? 256 : 128 * blocks_of(t));
         for (int kb = seg.kb0; kb < seg.kb1; ++kb, st.next(n_stages), acc.next(2)) {
           const uint32_t s = st.i, b = acc.i;
-          if (!bar_wait(&full[s], st.phase) || !bar_wait(&d_empty[b], acc.phase ^ 1)) {
-            give_up();
-            break;
-          }
+          bar_wait(&full[s], st.phase, guard);
+          bar_wait(&d_empty[b], acc.phase ^ 1, guard);
           // what cp.async wrote is read by the tensor core's proxy
           if (gather) fence_async();
           tc_fence_after();
-          __syncwarp();
           const uint64_t ad = sw128_desc(s32(tsm + s * kStage));
           const uint64_t bd = sw128_desc(s32(tsm + s * kStage + kABytes));
           tc_mma_block<CG>(tmem + b * 256, ad, bd, idesc);
@@ -205,16 +200,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc_commit<CG>(&d_full[b]);
         }
       }
+      if (guard.aborted()) {  // else the epilogue has waited for every MMA
+        tc_commit<CG>(drain);
+        bar_wait_for(drain, 0);
+      }
     } else if (warp == 1 && gather) {
       // ============================ second CTA: its activations have landed
       Ring st;
-      while (!*abort_flag && walk.take(seg))
+      while (!guard.aborted() && walk.take(seg))
         for (int kb = seg.kb0; kb < seg.kb1; ++kb, st.next(n_stages)) {
-          if (!bar_wait(&landed[st.i], st.phase)) {
-            give_up();
-            break;
-          }
+          bar_wait(&landed[st.i], st.phase, guard);
           fence_async();
+          __syncwarp();
           if (lane == 0) bar_arrive_first(&full[st.i]);
         }
     } else if (warp >= 2 && gather) {
@@ -224,7 +221,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int r0 = 4 * (warp - 2) + lane / 8, chunk = lane & 7;
       uint64_t *done = rank == 0 ? full : landed;
       Ring st;
-      while (!*abort_flag && walk.take(seg)) {
+      while (!guard.aborted() && walk.take(seg)) {
         const Fp8Tile t = my_tile(seg.tile);
         int row[kJ];  // a bad one (flagged) reads row 0
 #pragma unroll
@@ -232,10 +229,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           row[j] = 8 * j + r0 < t.rows ? max(0, fp8_x_row(a, t.row0 + 8 * j + r0)) : -1;
         for (int kb = seg.kb0; kb < seg.kb1; ++kb, st.next(n_stages)) {
           const uint32_t s = st.i;
-          if (!bar_wait(&empty[s], st.phase ^ 1)) {
-            give_up();
-            break;
-          }
+          bar_wait(&empty[s], st.phase ^ 1, guard);
           const uint32_t k0 = kb * 128 + chunk * 16;
           const uint8_t *src = a.xq + (k0 < a.K ? k0 : 0);
           const int bytes = k0 < a.K ? 16 : 0;
@@ -260,12 +254,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t col0 = (uint32_t)(quarter * 32) << 16 | (kSplitBlock ? 64 : 128) * half;
     constexpr uint32_t kCol1 = SWIGLU ? 128 : 64;  // from chunk 0 to chunk 2
     uint32_t g = 0, npair = 0;  // accumulators, and meetings of the pair, so far
-    auto meet = [&]() -> bool {
+    auto meet = [&]() {
       __syncwarp();
       if (lane == 0) bar_arrive(&pair[quarter]);
-      const bool ok = bar_wait(&pair[quarter], npair++ & 1);
-      if (!ok) give_up();
-      return ok;
+      bar_wait(&pair[quarter], npair++ & 1, guard);
     };
     auto release = [&](uint32_t b) {
       tc_fence_before();
@@ -276,20 +268,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     };
     uint32_t n_ex = 0;
-    while (!*abort_flag && walk.take(seg)) {
+    while (!guard.aborted() && walk.take(seg)) {
       const Fp8Tile t = my_tile(seg.tile);
       const bool warp_live = quarter * 32 < t.rows && (kSplitBlock || half < blocks_of(t));
       const bool live = warp_live && m < t.rows;
       float2 acc[16 * kChunks];
 #pragma unroll
       for (int i = 0; i < 16 * kChunks; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      bool ok = true;
       if (!warp_live) {
-        for (int kb = seg.kb0; ok && kb < seg.kb1; ++kb, ++g) {
-          ok = bar_wait(&d_full[g & 1], (g / 2) & 1);
-          if (ok) release(g & 1);
+        for (int kb = seg.kb0; kb < seg.kb1; ++kb, ++g) {
+          bar_wait(&d_full[g & 1], (g / 2) & 1, guard);
+          release(g & 1);
         }
-        if (!ok) give_up();
       } else {
         const int r = t.row0 + min(m, t.rows - 1);
         const size_t blk = kSplitBlock ? t.nt : 2 * t.nt + half;
@@ -307,14 +297,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // thread's loads), the next pair issued as registers come free -- across
         // the blocks too, so that a load's latency lies under the FMAs before it.
         float v0[32], v1[32];
-        ok = bar_wait(&d_full[g & 1], (g / 2) & 1);
-        if (ok) {
-          tc_fence_after();
-          const uint32_t base = tmem + col0 + (g & 1) * 256;
-          tc_ld32(base, v0);
-          tc_ld32(base + 32, v1);
-        }
-        for (int kb = seg.kb0; ok && kb < seg.kb1; ++kb, ++g) {
+        bar_wait(&d_full[g & 1], (g / 2) & 1, guard);
+        tc_fence_after();
+        tc_ld32(tmem + col0 + (g & 1) * 256, v0);
+        tc_ld32(tmem + col0 + (g & 1) * 256 + 32, v1);
+        for (int kb = seg.kb0; kb < seg.kb1; ++kb, ++g) {
           const uint32_t base = tmem + col0 + (g & 1) * 256;
           const float s0 = sx * sa, s1 = SWIGLU ? sx * sb : s0;
           const int kn = min(kb + 1, seg.kb1 - 1);
@@ -336,16 +323,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const bool more = kb + 1 < seg.kb1;
           const uint32_t next = tmem + col0 + ((g + 1) & 1) * 256;
           if (more) {
-            ok = bar_wait(&d_full[(g + 1) & 1], ((g + 1) / 2) & 1);
+            bar_wait(&d_full[(g + 1) & 1], ((g + 1) / 2) & 1, guard);
             tc_fence_after();
-            if (ok) tc_ld32(next, v0);
+            tc_ld32(next, v0);
           }
           fma32(v1, kChunks - 1, s1);
-          if (more && ok) tc_ld32(next + 32, v1);
+          if (more) tc_ld32(next + 32, v1);
         }
-        if (!ok) give_up();
       }
-      if (!ok) break;
       // ---- a share of a tile: the last of its workers adds up all shares
       if (seg.kb1 - seg.kb0 < (int)a.nbk) {
         if (quarter * 32 >= t.rows) continue;  // both warps of the pair
@@ -362,7 +347,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           __stcg(mine + 32 * i,
                  make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y));
         __threadfence();
-        if (!meet()) break;
+        meet();
         uint32_t *count = a.sync + 4 * (seg.tile * CG + rank) + quarter;
         if (half == 0 && lane == 0) {
           __threadfence();
@@ -370,7 +355,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (last) atomicExch(count, 0u);
           last_part[quarter] = last;
         }
-        if (!meet()) break;
+        meet();
         if (!last_part[quarter]) continue;
         __threadfence();
 #pragma unroll
@@ -439,7 +424,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         float *e = ex + (n_ex++ & 1) * 256;
         e[128 * half + m] = amax;
-        if (!meet()) break;
+        meet();
         amax = fmaxf(amax, e[128 * (half ^ 1) + m]);
         float sc, inv;
         fp8_block_scale(amax, sc, inv);
@@ -484,7 +469,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 template <bool SWIGLU, int MT, int NH, int CG>
 cudaError_t run_tc(Fp8Args &a, cudaStream_t stream) {
   const int sms = fp8_ctas() / CG * CG;
-  fp8_set_tiles(a, SWIGLU ? a.nbn : (a.nbn + NH - 1) / NH);
+  fp8_set_tiles(a, SWIGLU ? a.nbn : (a.nbn + NH - 1) / NH, sms / CG);
   const uint32_t quarters = ((a.R < 128 ? a.R : 128) + 31) / 32;
   a.part_stride = (size_t)quarters * 8192;
   Fp8Maps maps;

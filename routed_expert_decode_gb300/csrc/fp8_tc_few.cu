@@ -66,15 +66,16 @@ struct Cols {
   }
 };
 
-template <bool SWIGLU, int MT>
+template <bool SWIGLU, int MT, int NB>
 __global__ void __launch_bounds__(kFewThreads, 1)
     k_fp8_few(const Fp8Args a, const __grid_constant__ Fp8Maps maps, const uint32_t n_stages,
               const int split_below) {
   pdl_trigger();
   extern __shared__ __align__(1024) uint8_t tsm_raw[];
   uint8_t *tsm = (uint8_t *)(((uintptr_t)tsm_raw + 1023) & ~(uintptr_t)1023);
-  constexpr uint32_t kXBytes = MT * 128, kStage = kXBytes + 2 * kWBytes;
-  constexpr uint32_t kAccs = 512 / (2 * MT);  // accumulators in flight
+  static_assert(!SWIGLU || NB == 2, "gate and up");
+  constexpr uint32_t kXBytes = MT * 128, kStage = kXBytes + NB * kWBytes;
+  constexpr uint32_t kAccs = 256 / MT;        // accumulators in flight
   constexpr int kC = MT / 2;                  // rows of an epilogue warp
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t *ctrl = tsm + n_stages * kStage;
@@ -83,7 +84,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   uint64_t *d_full = empty + kMaxStages;  // [kAccs] accumulator and its row scales written
   uint64_t *d_empty = d_full + kAccs;   // [kAccs] ... read
   uint64_t *meet_bar = d_empty + kAccs;  // [2] the four epilogue warps of a row half
-  uint32_t *tmem_holder = (uint32_t *)(meet_bar + 2);
+  uint64_t *drain = meet_bar + 2;       // the MMAs of an aborted call
+  uint32_t *tmem_holder = (uint32_t *)(drain + 1);
   volatile int *abort_flag = (volatile int *)(tmem_holder + 1);
   volatile int *last_part = (volatile int *)(tmem_holder + 2);  // [2]
   float *xsc = (float *)(ctrl + 512);                           // [kAccs][MT] row scales
@@ -106,6 +108,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       bar_init(&d_empty[i], 8);
     }
     for (int i = 0; i < 2; ++i) bar_init(&meet_bar[i], 4);
+    bar_init(drain, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -122,63 +125,61 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   fp8_warm(a);
   pdl_wait();
   const RowTiles rt = fp8_row_tiles<MT>(a, tiles_sm);
-  Walk walk(rt.total * (int)a.n_tiles, (int)a.nbk, (int)blockIdx.x, (int)gridDim.x, split_below);
+  Walk walk(rt.total * (int)a.n_tiles, a, (int)blockIdx.x, (int)gridDim.x, split_below);
   Seg seg;
-  auto give_up = [&]() {
-    atomicOr(a.err, kErrTimeout);
-    *abort_flag = 1;
-  };
+  const Guard guard{a.err, abort_flag};
   // weight blocks that a tile has: the last of an odd number stands alone
-  auto blocks_of = [&](const Fp8Tile &t) { return SWIGLU ? 2 : min(2, (int)a.nbn - t.nt * 2); };
+  auto blocks_of = [&](const Fp8Tile &t) { return SWIGLU ? 2 : min(NB, (int)a.nbn - t.nt * NB); };
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ============================ weights (and activations in order)
-      Ring st;
-      while (!*abort_flag && walk.take(seg)) {
-        const Fp8Tile t = fp8_tile<MT>(a, rt, seg.tile);
-        const int nb = blocks_of(t);
-        const uint32_t bytes = nb * kWBytes + (gather ? 0 : kXBytes);
-        for (int kb = seg.kb0; kb < seg.kb1; ++kb, st.next(n_stages)) {
-          const uint32_t s = st.i;
-          if (!bar_wait(&empty[s], st.phase ^ 1)) {  // the first use passes
-            give_up();
-            break;
-          }
-          uint8_t *buf = tsm + s * kStage, *dst = buf + kXBytes;
-          bar_expect(&full[s], bytes);
-          for (int h = 0; h < nb; ++h)
-            tma_w<1>(dst + h * kWBytes, &maps.w[SWIGLU ? h : 0], kb * 128,
-                     (SWIGLU ? t.nt : t.nt * 2 + h) * 128, t.e, &full[s]);
-          if (!gather) tma_x<1>(buf, &maps.x, kb * 128, t.row0, &full[s]);
-        }
+    // ============================ weights (and activations in order)
+    Ring st;
+    while (!guard.aborted() && walk.take(seg)) {
+      const Fp8Tile t = fp8_tile<MT>(a, rt, seg.tile);
+      const int nb = blocks_of(t);
+      const uint32_t bytes = nb * kWBytes + (gather ? 0 : kXBytes);
+      for (int kb = seg.kb0; kb < seg.kb1; ++kb, st.next(n_stages)) {
+        const uint32_t s = st.i;
+        bar_wait(&empty[s], st.phase ^ 1, guard);  // the first use passes
+        __syncwarp();
+        if (guard.aborted()) break;
+        if (lane) continue;
+        uint8_t *buf = tsm + s * kStage, *dst = buf + kXBytes;
+        bar_expect(&full[s], bytes);
+        for (int h = 0; h < nb; ++h)
+          tma_w<1>(dst + h * kWBytes, &maps.w[SWIGLU ? h : 0], kb * 128,
+                   (SWIGLU ? t.nt : t.nt * NB + h) * 128, t.e, &full[s]);
+        if (!gather) tma_x<1>(buf, &maps.x, kb * 128, t.row0, &full[s]);
       }
-      // the stages still in use: leave with no copy in flight
-      for (uint32_t i = 0; i < n_stages; ++i, st.next(n_stages))
-        if (!bar_wait(*abort_flag ? &full[st.i] : &empty[st.i], st.phase ^ 1)) give_up();
     }
+    // the stages still in use: leave with no copy in flight
+    for (uint32_t i = 0; i < n_stages; ++i, st.next(n_stages))
+      if (!bar_wait_for(*abort_flag ? &full[st.i] : &empty[st.i], st.phase ^ 1))
+        atomicOr(a.err, kErrTimeout);
   } else if (warp == 1) {
     // ============================ MMA issuer
     Ring st, acc;
     const uint32_t idesc = idesc_for<1>(MT);
-    while (!*abort_flag && walk.take(seg)) {
+    while (!guard.aborted() && walk.take(seg)) {
       const int nb = blocks_of(fp8_tile<MT>(a, rt, seg.tile));
       for (int kb = seg.kb0; kb < seg.kb1; ++kb, st.next(n_stages), acc.next(kAccs)) {
-        if (!bar_wait(&full[st.i], st.phase) || !bar_wait(&d_empty[acc.i], acc.phase ^ 1)) {
-          give_up();
-          break;
-        }
+        bar_wait(&full[st.i], st.phase, guard);
+        bar_wait(&d_empty[acc.i], acc.phase ^ 1, guard);
         if (gather) fence_async();  // cp.async's writes, read by the tensor core's proxy
         tc_fence_after();
         __syncwarp();
         const uint32_t buf = s32(tsm + st.i * kStage);
         const uint64_t xd = sw128_desc(buf), wd = sw128_desc(buf + kXBytes);
-        const uint32_t d = tmem + acc.i * 2 * MT;
+        const uint32_t d = tmem + acc.i * NB * MT;
         tc_mma_block<1>(d, wd, xd, idesc);
-        if (nb == 2) tc_mma_block<1>(d + MT, wd + (kWBytes >> 4), xd, idesc);
+        if (NB == 2 && nb == 2) tc_mma_block<1>(d + MT, wd + (kWBytes >> 4), xd, idesc);
         tc_commit<1>(&empty[st.i]);
         tc_commit<1>(&d_full[acc.i]);
       }
+    }
+    if (guard.aborted()) {  // else the epilogue has waited for every MMA
+      tc_commit<1>(drain);
+      bar_wait_for(drain, 0);
     }
   } else if (warp == 2) {
     if (gather) {
@@ -187,17 +188,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       constexpr int kJ = MT / 4;
       const int r0 = lane / 8, chunk = lane & 7;
       Ring st;
-      while (!*abort_flag && walk.take(seg)) {
+      while (!guard.aborted() && walk.take(seg)) {
         const Fp8Tile t = fp8_tile<MT>(a, rt, seg.tile);
         int row[kJ];  // a bad one (flagged) reads row 0
 #pragma unroll
         for (int j = 0; j < kJ; ++j)
           row[j] = 4 * j + r0 < t.rows ? max(0, fp8_x_row(a, t.row0 + 4 * j + r0)) : -1;
         for (int kb = seg.kb0; kb < seg.kb1; ++kb, st.next(n_stages)) {
-          if (!bar_wait(&empty[st.i], st.phase ^ 1)) {
-            give_up();
-            break;
-          }
+          bar_wait(&empty[st.i], st.phase ^ 1, guard);
           const uint32_t k0 = kb * 128 + chunk * 16;
           const uint8_t *src = a.xq + (k0 < a.K ? k0 : 0);
           const int bytes = k0 < a.K ? 16 : 0;
@@ -218,7 +216,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // ============================ row scales, one block of K ahead in registers
     constexpr int kR = MT / 32;
     Ring acc;
-    while (!*abort_flag && walk.take(seg)) {
+    while (!guard.aborted() && walk.take(seg)) {
       const Fp8Tile t = fp8_tile<MT>(a, rt, seg.tile);
       const float *xs[kR];
       float next[kR];
@@ -235,10 +233,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           v[i] = next[i];
           next[i] = xs[i][min(kb + 1, seg.kb1 - 1)];
         }
-        if (!bar_wait(&d_empty[acc.i], acc.phase ^ 1)) {
-          give_up();
-          break;
-        }
+        bar_wait(&d_empty[acc.i], acc.phase ^ 1, guard);
 #pragma unroll
         for (int i = 0; i < kR; ++i) xsc[acc.i * MT + lane + 32 * i] = v[i];
         __syncwarp();
@@ -251,27 +246,25 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const int f = quarter * 32 + lane;  // feature of a weight block, TMEM lane
     Ring dr;
     uint32_t nmeet = 0, nred = 0;
-    auto meet = [&]() -> bool {  // the four warps of this row half
+    auto meet = [&]() {  // the four warps of this row half
       __syncwarp();
       if (lane == 0) bar_arrive(&meet_bar[c]);
-      const bool ok = bar_wait(&meet_bar[c], nmeet++ & 1);
-      if (!ok) give_up();
-      return ok;
+      bar_wait(&meet_bar[c], nmeet++ & 1, guard);
     };
     const uint32_t col0 = ((uint32_t)(quarter * 32) << 16) + c * kC;
-    while (!*abort_flag && walk.take(seg)) {
+    while (!guard.aborted() && walk.take(seg)) {
       const Fp8Tile t = fp8_tile<MT>(a, rt, seg.tile);
       const int rows = t.rows - c * kC;  // live rows of this warp
       const int nb = blocks_of(t);
-      float2 acc[2][kC / 2];  // pairs of rows
+      float2 acc[NB][kC / 2];  // pairs of rows
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < NB; ++h)
 #pragma unroll
         for (int i = 0; i < kC / 2; ++i) acc[h][i] = make_float2(0.0f, 0.0f);
       // the segment's blocks of K with NC columns read of each accumulator
-      auto add = [&](auto nc) -> bool {
+      auto add = [&](auto nc) {
         constexpr int NC = decltype(nc)::n;
-        const size_t blk = SWIGLU ? t.nt : 2 * t.nt;
+        const size_t blk = SWIGLU ? t.nt : NB * t.nt;
         const float *wa = a.wsc[0] + ((size_t)t.e * a.nbn + blk) * a.nbk;
         const float *wb = SWIGLU ? a.wsc[1] + ((size_t)t.e * a.nbn + blk) * a.nbk
                           : nb == 2 ? wa + a.nbk : wa;
@@ -279,26 +272,27 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         for (int kb = seg.kb0; kb < seg.kb1; ++kb) {
           const float s[2] = {sa, sb};
           const int kn = min(kb + 1, seg.kb1 - 1);
-          sa = wa[kn], sb = wb[kn];  // on the way while this block is added
-          if (!bar_wait(&d_full[dr.i], dr.phase)) return false;
+          sa = wa[kn];  // on the way while this block is added
+          bar_wait(&d_full[dr.i], dr.phase, guard);
           tc_fence_after();
-          Cols<NC> v[2];
-          const uint32_t base = tmem + col0 + dr.i * 2 * MT;
+          if (NB == 2) sb = wb[kn];
+          Cols<NC> v[NB];
+          const uint32_t base = tmem + col0 + dr.i * NB * MT;
           v[0].load(base);
-          v[1].load(base + MT);
+          if (NB == 2) v[NB - 1].load(base + MT);
           float4 x[NC / 4];
           const float4 *xp = (const float4 *)(xsc + dr.i * MT + c * kC);
 #pragma unroll
           for (int i = 0; i < NC / 4; ++i) x[i] = xp[i];
           asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
           v[0].tie();
-          v[1].tie();
+          if (NB == 2) v[NB - 1].tie();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) bar_arrive(&d_empty[dr.i]);
           dr.next(kAccs);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < NB; ++h) {
             const float2 s2 = make_float2(s[h], s[h]);
 #pragma unroll
             for (int i = 0; i < NC / 2; ++i) {
@@ -309,22 +303,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
           }
         }
-        return true;
       };
-      bool ok = true;
       if (rows <= 0) {
-        for (int kb = seg.kb0; ok && kb < seg.kb1; ++kb, dr.next(kAccs)) {
-          ok = bar_wait(&d_full[dr.i], dr.phase);
-          if (ok && lane == 0) bar_arrive(&d_empty[dr.i]);
+        for (int kb = seg.kb0; kb < seg.kb1; ++kb, dr.next(kAccs)) {
+          bar_wait(&d_full[dr.i], dr.phase, guard);
+          __syncwarp();
+          if (lane == 0) bar_arrive(&d_empty[dr.i]);
         }
       } else if (rows <= 8) {
-        ok = add(Int<8>());
+        add(Int<8>());
       } else {
-        ok = add(Int<kC>());
-      }
-      if (!ok) {
-        give_up();
-        break;
+        add(Int<kC>());
       }
       if (rows <= 0) continue;  // the four warps of this half alike
       // ---- a share of a tile: the last of its workers adds up all shares
@@ -338,12 +327,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         };
         float2 *mine = part((int)blockIdx.x);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < NB; ++h)
 #pragma unroll
           for (int i = 0; i < kC / 2; ++i)
             if (2 * i < rows) __stcg(mine + (h * (kC / 2) + i) * 32, acc[h][i]);
         __threadfence();
-        if (!meet()) break;
+        meet();
         uint32_t *count = a.sync + 4 * seg.tile + c;
         if (quarter == 0 && lane == 0) {
           __threadfence();
@@ -351,17 +340,18 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           if (last) atomicExch(count, 0u);
           last_part[c] = last;
         }
-        if (!meet()) break;
+        meet();
         if (!last_part[c]) continue;
         __threadfence();
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < NB; ++h)
 #pragma unroll
           for (int i = 0; i < kC / 2; ++i) acc[h][i] = make_float2(0.0f, 0.0f);
-        for (int p = 0; p < n; ++p) {
+#pragma unroll 4
+        for (int p = 0; p < n; ++p) {  // four shares' loads on the way together
           const float2 *src = part(c0 + p);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < NB; ++h)
 #pragma unroll
             for (int i = 0; i < kC / 2; ++i)
               if (2 * i < rows) {
@@ -375,8 +365,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       const int r0 = t.row0 + c * kC;
       if (!SWIGLU) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t n = (uint32_t)(t.nt * 2 + h) * 128 + f;
+        for (int h = 0; h < NB; ++h) {
+          const uint32_t n = (uint32_t)(t.nt * NB + h) * 128 + f;
           if (n >= a.N) continue;
           const size_t at = (size_t)r0 * a.ld + n;
           auto store = [&](auto *p, auto from) {
@@ -399,12 +389,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         for (int i = 0; i < kC; ++i) {
           if (i >= rows) break;  // past the code of the rows that are not there
           float &g = i & 1 ? acc[0][i / 2].y : acc[0][i / 2].x;
-          g = fp8_swiglu_value(g, i & 1 ? acc[1][i / 2].y : acc[1][i / 2].x);
+          g = fp8_swiglu_value(g, i & 1 ? acc[NB - 1][i / 2].y : acc[NB - 1][i / 2].x);
           const float m = g == g ? fabsf(g) : 0.0f;
           const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
           if (lane == 0) mx[quarter * MT + i] = __uint_as_float(w);
         }
-        if (!meet()) break;
+        meet();
         // lane i works out row i's scale
         float sc = 0.0f, inv = 0.0f;
         if (lane < rows && lane < kC) {
@@ -432,10 +422,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
 }
 
-template <bool SWIGLU, int MT>
+template <bool SWIGLU, int MT, int NB>
 cudaError_t run_few(Fp8Args &a, cudaStream_t stream) {
   const int sms = fp8_ctas();
-  fp8_set_tiles(a, SWIGLU ? a.nbn : (a.nbn + 1) / 2);
+  fp8_set_tiles(a, SWIGLU ? a.nbn : (a.nbn + NB - 1) / NB, sms);
   a.part_stride = (size_t)MT * 256;
   Fp8Maps maps;
   memset(&maps, 0, sizeof maps);
@@ -444,8 +434,8 @@ cudaError_t run_few(Fp8Args &a, cudaStream_t stream) {
       (SWIGLU && !byte_map(&maps.w[1], a.wq[1], a.K, a.N, a.E, 3, 128)))
     return cudaErrorInvalidValue;
   if (!SWIGLU) maps.w[1] = maps.w[0];
-  auto kern = k_fp8_few<SWIGLU, MT>;
-  const size_t stage = MT * 128 + 2 * (size_t)kWBytes;
+  auto kern = k_fp8_few<SWIGLU, MT, NB>;
+  const size_t stage = MT * 128 + NB * (size_t)kWBytes;
   const size_t rest = 1024 + 512 + 4 * (256 + 8 * MT) + fp8_tiles_smem(a.E);
   int ns = (int)((kSmemLimit - rest) / stage);
   if (ns > kMaxStages) ns = kMaxStages;
@@ -453,16 +443,26 @@ cudaError_t run_few(Fp8Args &a, cudaStream_t stream) {
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
+  // Tiles are split along K only when they leave three SMs of four idle: 64 SMs
+  // already draw 5.4 TB/s, and under a saturated HBM each of the split's round trips
+  // (shares out, count, shares in) takes ~3 us.  16 tiles of 48 blocks: 10.5 us split,
+  // 22.4 whole; 64 tiles: 25.7 split, 23.6 whole.
   return launch_k(kern, sms, kFewThreads, smem, stream, true, a, maps, (uint32_t)ns,
-                  0);
+                  sms / 4);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_few(Fp8Args &a, bool swiglu, cudaStream_t stream) {
   const uint64_t R = a.R, E = a.E;
-  if (R <= 32 * E) return swiglu ? run_few<true, 32>(a, stream) : run_few<false, 32>(a, stream);
-  return swiglu ? run_few<true, 64>(a, stream) : run_few<false, 64>(a, stream);
+  if (R > 32 * E) return swiglu ? run_few<true, 64, 2>(a, stream) : run_few<false, 64, 2>(a, stream);
+  if (swiglu) return run_few<true, 32, 2>(a, stream);
+  // At most this many pairs of weight blocks have rows.  Few rounds of tiles go out
+  // more evenly one block a tile (one token's down projection, 192 pairs: 22.0
+  // against 23.1 us); with many rounds a pair shares a tile's fixed work.
+  const uint64_t pairs = (R < E ? R : E) * ((a.nbn + 1) / 2);
+  return pairs <= 4 * (uint64_t)fp8_ctas() ? run_few<false, 32, 1>(a, stream)
+                                           : run_few<false, 32, 2>(a, stream);
 }
 
 }  // namespace moe

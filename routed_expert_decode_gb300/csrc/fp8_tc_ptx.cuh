@@ -40,8 +40,20 @@ __device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-// bounded by a clock budget and a count
-__device__ __forceinline__ bool bar_wait_long(uint64_t *b, uint32_t parity) {
+// What a wait that runs out does: it flags the call and sets the CTA's abort flag,
+// after which every wait returns at once.  The work goes on to the end of the
+// segment on whatever the buffers hold, so that a warp's lanes never part in front
+// of a warp-wide instruction, and the roles' loops end there.
+struct Guard {
+  uint32_t *err;
+  volatile int *abort_flag;
+  // by a whole warp
+  __device__ __forceinline__ bool aborted() const {
+    return __any_sync(0xffffffffu, *abort_flag != 0);
+  }
+};
+// bounded by a clock budget and a count; false: it ran out
+__device__ __forceinline__ bool bar_wait_for(uint64_t *b, uint32_t parity) {
   const long long t0 = clock64();
   for (int i = 0; i < kSpin; ++i) {
     if (bar_try(b, parity)) return true;
@@ -49,8 +61,15 @@ __device__ __forceinline__ bool bar_wait_long(uint64_t *b, uint32_t parity) {
   }
   return false;
 }
-__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity) {
-  return bar_try(b, parity) || bar_wait_long(b, parity);
+__device__ __forceinline__ void bar_wait(uint64_t *b, uint32_t parity, const Guard &g) {
+  if (bar_try(b, parity) || *g.abort_flag) return;
+  const long long t0 = clock64();
+  for (int i = 0; i < kSpin && !*g.abort_flag; ++i) {
+    if (bar_try(b, parity)) return;
+    if (clock64() - t0 > kWaitCycles) break;
+  }
+  if (!*g.abort_flag) atomicOr(g.err, kErrTimeout);
+  *g.abort_flag = 1;
 }
 // arrive on the same barrier of the pair's first CTA
 __device__ __forceinline__ void bar_arrive_first(uint64_t *b) {
@@ -227,12 +246,13 @@ struct Walk {
   int n_all, share, kbs, grid;  // tiles, K blocks per worker of the split tiles, per tile
   int pos, end, next;
   // the last, partial round is split if it has fewer than split_below tiles
-  __device__ Walk(int n_all_, int kbs_, int worker, int workers, int split_below)
-      : n_all(n_all_), kbs(kbs_), grid(workers) {
+  __device__ Walk(int n_all_, const Fp8Args &a, int worker, int workers, int split_below)
+      : n_all(n_all_), kbs((int)a.nbk), grid(workers) {
     // 32 bits hold them: below 256 split tiles of at most 2^17 K blocks
-    const int rest = n_all % grid, split = rest < split_below ? rest : 0;
+    const int rest = n_all - grid * (int)quotient(n_all, grid, a.workers_inv);
+    const int split = rest < split_below ? rest : 0;
     const int items = split * kbs;
-    share = max((items + grid - 1) / grid, min(kMinShare, kbs));
+    share = max((int)quotient(items + grid - 1, grid, a.workers_inv), min(kMinShare, kbs));
     pos = min(items, worker * share);
     end = min(items, pos + share);
     next = split + worker;

@@ -23,6 +23,7 @@ struct Fp8Args {
   float *hs;
   int odt;
   uint32_t n_tiles, n_tiles_inv;  // column tiles of an expert, floor((2^32 - 1) / that)
+  uint32_t workers_inv;           // the same of the CTAs (pairs) that share the tiles
   uint32_t *err, *sync;
   float *part;         // partial sums of split tiles
   size_t part_stride;  // floats per part
@@ -34,7 +35,7 @@ struct Fp8Args {
 __device__ __forceinline__ void fp8_warm(const Fp8Args &a) {
   asm volatile("" ::"r"(a.E), "r"(a.N), "r"(a.nbn), "r"(a.nbk), "r"(a.R), "r"(a.top_k), "l"(a.xq),
                "l"(a.xs), "l"(a.off), "l"(a.perm), "l"(a.wsc[0]), "l"(a.wsc[1]), "l"(a.out),
-               "l"(a.hs), "r"(a.n_tiles), "r"(a.n_tiles_inv), "l"(a.err), "l"(a.sync),
+               "l"(a.hs), "r"(a.n_tiles), "r"(a.n_tiles_inv), "r"(a.workers_inv), "l"(a.err), "l"(a.sync),
                "l"(a.part));
   auto prefetch = [](const int32_t *p, uint32_t n) {
     const uint32_t i = threadIdx.x * 32;
@@ -69,39 +70,47 @@ __device__ __forceinline__ RowTiles fp8_row_tiles(const Fp8Args &a, int *sm) {
     const int lane = threadIdx.x;
     const int per = (E + 31) / 32, b = min(E, lane * per), e1 = min(E, b + per);
     auto off = [&](int e) { return a.off ? a.off[e] : e == 0 ? 0 : R; };
-    int at = off(b), tiles = 0;
+    auto warp_scan = [&](int v) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      return v;
+    };
+    int at = off(b), tiles = 0, incl;
     bool bad = at < 0 || at > R;
     if (per <= 8) {
-      int next[8];
+      int next[8], before[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) next[i] = b + i < e1 ? off(b + i + 1) : 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 8; ++i) {
+        before[i] = tiles;
         if (b + i < e1) {
           s_off[b + i] = at;
-          s_tile[b + i] = tiles;  // within the lane's run so far
           bad |= next[i] < at || next[i] > R;
           tiles += (max(next[i] - at, 0) + MT - 1) / MT;
           at = next[i];
         }
+      }
+      incl = warp_scan(tiles);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (b + i < e1) s_tile[b + i] = incl - tiles + before[i];
     } else {
 #pragma unroll 8
       for (int e = b; e < e1; ++e) {
         const int next = off(e + 1);
         s_off[e] = at;
-        s_tile[e] = tiles;
+        s_tile[e] = tiles;  // within the lane's run so far
         bad |= next < at || next > R;
         tiles += (max(next - at, 0) + MT - 1) / MT;
         at = next;
       }
+      incl = warp_scan(tiles);
+      for (int e = b; e < e1; ++e) s_tile[e] += incl - tiles;
     }
-    int incl = tiles;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    for (int e = b; e < e1; ++e) s_tile[e] += incl - tiles;
     bad = __any_sync(0xffffffffu, bad);
     if (lane == 31) {
       s_off[E] = at;
@@ -122,19 +131,26 @@ struct Fp8Tile {
   int e, row0, rows, nt;  // expert, first output row, live rows, column tile
 };
 
-// tile v of total * n_tiles: experts in order, an expert's column tiles one
+// v / d with inv = floor((2^32 - 1) / d): the product's high word is at most one short
+__device__ __forceinline__ uint32_t quotient(uint32_t v, uint32_t d, uint32_t inv) {
+  const uint32_t q = __umulhi(v, inv);
+  return v - q * d >= d ? q + 1 : q;
+}
+
+// By a whole warp: tile v of total * n_tiles: experts in order, an expert's column tiles one
 // after another, its row tiles innermost (they share the weights)
 template <int MT>
 __device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Args &a, const RowTiles &rt, int v) {
-  // expert e's tiles are [tile[e] * n_tiles, tile[e+1] * n_tiles); v / n_tiles by the
-  // host's reciprocal, whose quotient is at most one short
-  int q = (int)__umulhi((uint32_t)v, a.n_tiles_inv);
-  if (v - q * (int)a.n_tiles >= (int)a.n_tiles) ++q;
-  int lo = 0, hi = (int)a.E;  // largest e with tile[e] <= q (experts without rows share a prefix)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (rt.tile[mid] <= q) lo = mid; else hi = mid;
-  }
+  // expert e's tiles are [tile[e] * n_tiles, tile[e+1] * n_tiles)
+  const int q = (int)quotient((uint32_t)v, a.n_tiles, a.n_tiles_inv);
+  // the largest e with tile[e] <= q (experts without rows share a prefix): a run of
+  // experts a lane, then a lane an expert of that run
+  const int lane = threadIdx.x & 31, E = (int)a.E, per = (E + 31) >> 5;
+  const int first = lane * per;
+  const int run = __popc(__ballot_sync(0xffffffffu, first < E && rt.tile[min(first, E)] <= q)) - 1;
+  const int e = run * per + lane;
+  const int lo = run * per - 1 +
+                 __popc(__ballot_sync(0xffffffffu, lane < per && e < E && rt.tile[min(e, E)] <= q));
   const int mt = rt.tile[lo + 1] - rt.tile[lo];
   const int local = v - rt.tile[lo] * (int)a.n_tiles;
   Fp8Tile t;
@@ -148,9 +164,10 @@ __device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Args &a, const RowTiles &rt
 
 inline size_t fp8_tiles_smem(uint32_t E) { return 4 * (2 * ((size_t)E + 1) + 2); }
 
-inline void fp8_set_tiles(Fp8Args &a, uint32_t n_tiles) {
+inline void fp8_set_tiles(Fp8Args &a, uint32_t n_tiles, uint32_t workers) {
   a.n_tiles = n_tiles;
   a.n_tiles_inv = 0xffffffffu / n_tiles;
+  a.workers_inv = 0xffffffffu / workers;
 }
 
 // store one output value of the product
