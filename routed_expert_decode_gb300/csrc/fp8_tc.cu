@@ -490,8 +490,8 @@ cudaError_t run_tc(Fp8Args &a, cudaStream_t stream) {
   const size_t smem = rest + ns * stage;
   const int workers = sms / CG;
   const int split_below = workers * 7 / 8;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static int set[kMaxDevices];
+  const cudaError_t e = allow_smem(kern, smem, set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = sms;

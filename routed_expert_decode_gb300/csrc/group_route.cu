@@ -429,8 +429,8 @@ cudaError_t run_route(const GrArgs &a, uint32_t grid, cudaStream_t stream) {
   const uint32_t threads = few ? 32 * (a.T > 8 ? a.T : 8) : kGrThreads;
   const size_t smem = 4 * ((size_t)kGrWarps * 32 + threads * NPER +
                            (few ? 0 : (size_t)E * (kGrMaskWords + 1) + 32));
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static int set[kMaxDevices];
+  const cudaError_t e = allow_smem(kern, smem, set);
   if (e != cudaSuccess) return e;
   if (grid == 1) return launch_k(kern, 1, threads, smem, stream, true, a, few);
   GrArgs args = a;

@@ -94,23 +94,29 @@ def _stream(stream, t: torch.Tensor):
 
 def _rows2d(t: torch.Tensor, name: str):
     """(pointer, dtype code, row stride) of a 2-d CUDA tensor with consecutive columns."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
     dt = DTYPES.get(t.dtype)
-    if dt is None:
-        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    shape, (ld, step) = t.shape, t.stride()
-    if step != 1 and shape[1] > 1:
-        raise ValueError(f"{name} must have consecutive columns")
-    return t.data_ptr(), dt, ld if shape[0] > 1 else shape[1]
+    ld, step = t.stride()
+    if dt is None or step != 1 or ld < t.shape[1] or not t.is_cuda:
+        rows, cols = t.shape
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dt is None:
+            raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+        if step != 1 and cols > 1:
+            raise ValueError(f"{name} must have consecutive columns")
+        if ld < cols:
+            if rows > 1:
+                raise ValueError(f"{name}'s rows must not overlap")
+            ld = cols
+    return t.data_ptr(), dt, ld
 
 
 def _plane(t: torch.Tensor, dtypes, shape, name: str) -> int:
     """Pointer of a contiguous CUDA tensor of one of the dtypes and this shape."""
-    if not t.is_cuda or t.dtype not in dtypes or not t.is_contiguous() or t.shape != shape:
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtypes[0]} and shape "
-                         f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.is_cuda:
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtypes[0]} and shape "
+                     f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 _CODES = (torch.float8_e4m3fn, torch.uint8)
@@ -120,7 +126,8 @@ _U8 = (torch.uint8,)
 
 
 def _ws(ws: torch.Tensor):
-    return _plane(ws, _U8, (ws.numel(),), "ws"), ws.numel()
+    n = ws.numel()
+    return _plane(ws, _U8, (n,), "ws"), n
 
 
 # ------------------------------------------------------------------ router
@@ -145,7 +152,7 @@ def group_route(router: MoeRouter, logits, bias: Optional[torch.Tensor], idx, w,
         raise ValueError(f"logits must have {router.n_expert} columns, got {E}")
     lp, dt, ld = _rows2d(logits, "logits")
     wsp, wsn = _ws(ws)
-    st = lib().moe_group_route(
+    st = (_lib or lib()).moe_group_route(
         ctypes.byref(router), lp, dt, ld,
         None if bias is None else _plane(bias, _F32, (E,), "bias"), T,
         _plane(idx, _I32, (T, k), "idx"), _plane(w, _F32, (T, k), "w"),
@@ -161,7 +168,7 @@ def quantize(x, q, scale, stream=None) -> None:
     scales ``scale`` [T, ceil(d / 128)]."""
     T, d = x.shape
     xp, dt, ld = _rows2d(x, "x")
-    st = lib().moe_fp8_quantize(xp, dt, ld, T, d, _plane(q, _CODES, (T, d), "q"),
+    st = (_lib or lib()).moe_fp8_quantize(xp, dt, ld, T, d, _plane(q, _CODES, (T, d), "q"),
                                 _plane(scale, _F32, (T, blocks(d)), "scale"),
                                 _stream(stream, x))
     if st:
@@ -207,7 +214,7 @@ def product(w: Mat, xq, xs, out, ws, off=None, perm=None, top_k: int = 1, stream
     op, dt, ld = _rows2d(out, "out")
     x = _activation(w, xq, xs, R, off, perm, top_k)
     wsp, wsn = _ws(ws)
-    st = lib().moe_fp8_product(w.ref, w.E, N, w.K, ctypes.byref(x), op, dt, ld, wsp, wsn,
+    st = (_lib or lib()).moe_fp8_product(w.ref, w.E, N, w.K, ctypes.byref(x), op, dt, ld, wsp, wsn,
                                _stream(stream, out))
     if st:
         _check("moe_fp8_product", st)
@@ -222,7 +229,7 @@ def swiglu(gate: Mat, up: Mat, xq, xs, hq, hs, ws, off=None, perm=None, top_k: i
         raise ValueError("gate and up must have the same shape")
     x = _activation(gate, xq, xs, R, off, perm, top_k)
     wsp, wsn = _ws(ws)
-    st = lib().moe_fp8_swiglu(gate.ref, up.ref, gate.E, gate.N, gate.K, ctypes.byref(x),
+    st = (_lib or lib()).moe_fp8_swiglu(gate.ref, up.ref, gate.E, gate.N, gate.K, ctypes.byref(x),
                               _plane(hq, _CODES, (R, gate.N), "hq"),
                               _plane(hs, _F32, (R, blocks(gate.N)), "hs"), wsp, wsn,
                               _stream(stream, hq))
@@ -245,7 +252,7 @@ def combine(o, w, pos, y, shared=None, stream=None) -> None:
         sp, sdt, lds = _rows2d(shared, "shared")
         if sdt != dt:
             raise ValueError("shared must have o's type")
-    st = lib().moe_fp8_combine(op, dt, ldo, R, _plane(w, _F32, (T, k), "w"),
+    st = (_lib or lib()).moe_fp8_combine(op, dt, ldo, R, _plane(w, _F32, (T, k), "w"),
                                _plane(pos, _I32, (T, k), "pos"), T, k, d, sp, lds, yp, ydt, ldy,
                                _stream(stream, y))
     if st:
