@@ -66,7 +66,8 @@ extern "C" {
 
 size_t moe_group_route_workspace_size(const moe_router *r, uint32_t T) {
   if (!router_ok(r)) return 0;
-  return group_route_ws(*r, T);
+  (void)T;
+  return group_route_ws(*r);
 }
 
 moe_status moe_group_route(const moe_router *r, const void *logits, moe_dtype dt, size_t ld,
@@ -82,7 +83,7 @@ moe_status moe_group_route(const moe_router *r, const void *logits, moe_dtype dt
       return MOE_ERR_INVALID_ARG;
   }
   if ((uint64_t)T * r->top_k > (1u << 30)) return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < group_route_ws(*r, T)) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < group_route_ws(*r)) return MOE_ERR_WORKSPACE;
   return status_of(launch_group_route(*r, logits, dt, ld, bias, T, idx, w, off, perm, pos, ws,
                                       (cudaStream_t)stream));
 }

@@ -20,7 +20,7 @@ __host__ __device__ constexpr uint32_t fp8_blocks(uint32_t n) {
 
 // words of the workspace's counter area (moe.h) used by these operators, clear
 // of the layer's: zero between calls
-constexpr uint32_t kFp8RouteSync = 2064;     // [2]: CTAs in, CTAs out of the router's barrier
+constexpr uint32_t kFp8RouteSync = 2064;     // [2]: CTAs in, CTAs out of the permutation's barrier
 constexpr uint32_t kFp8TileSync = 2080;      // [kFp8MaxCtas * 4]: parts of a split tile done
 constexpr uint32_t kFp8MaxCtas = 256;
 static_assert(kQueueTcDown + 2 <= kFp8RouteSync &&
@@ -177,7 +177,7 @@ cudaError_t launch_fp8_combine(const void *o, int dt, size_t ldo, uint32_t R, co
                                const int32_t *pos, uint32_t T, uint32_t k, uint32_t d,
                                const void *shared, size_t lds, void *y, int ydt, size_t ldy,
                                cudaStream_t stream);
-size_t group_route_ws(const moe_router &r, uint32_t T);
+size_t group_route_ws(const moe_router &r);
 cudaError_t launch_group_route(const moe_router &r, const void *logits, int dt, size_t ld,
                                const float *bias, uint32_t T, int32_t *idx, float *w,
                                int32_t *off, int32_t *perm, int32_t *pos, void *ws,
