@@ -12,6 +12,7 @@ consecutive.  ``Layer`` runs them together as one routed layer.
 from __future__ import annotations
 
 import ctypes
+from dataclasses import dataclass
 from typing import Optional
 
 import torch
@@ -257,3 +258,95 @@ def combine(o, w, pos, y, shared=None, stream=None) -> None:
                                _stream(stream, y))
     if st:
         _check("moe_fp8_combine", st)
+
+
+# ------------------------------------------------------------------ convenience
+@dataclass
+class LayerOutput:
+    """What a layer call computed: its result and the buffers it went through (valid
+    until the layer's next call with as many tokens)."""
+    y: torch.Tensor
+    idx: torch.Tensor
+    w: torch.Tensor
+    off: torch.Tensor
+    perm: torch.Tensor
+    pos: torch.Tensor
+    xq: torch.Tensor
+    xs: torch.Tensor
+    hq: torch.Tensor
+    hs: torch.Tensor
+    o: torch.Tensor
+    shared: Optional[torch.Tensor]
+
+
+class Layer:
+    """One routed layer over fp8 weights on a device: group-limited routing, the experts'
+    SwiGLU and down products, the always-on shared expert, the weighted combine.
+
+    ``gate``, ``up`` [E, f, d] and ``down`` [E, d, f] are ``Mat``; ``shared`` is a
+    triple of one-expert ``Mat`` or None.  Buffers and the workspace are kept per number
+    of tokens and type, as ``moe.Layer`` keeps its own; calls that overlap need layers
+    (or streams' orders) of their own.
+    """
+
+    def __init__(self, router: MoeRouter, gate: Mat, up: Mat, down: Mat, shared=None):
+        if (gate.E, gate.N, gate.K) != (up.E, up.N, up.K) or \
+                (down.E, down.N, down.K) != (gate.E, gate.K, gate.N) or \
+                router.n_expert != gate.E:
+            raise ValueError("gate, up [E, f, d] and down [E, d, f] must be of the router's E "
+                             "experts")
+        if shared is not None:
+            sg, su, sd = shared
+            if (sg.E, sg.K) != (1, gate.K) or (su.E, su.N, su.K) != (1, sg.N, sg.K) or \
+                    (sd.E, sd.N, sd.K) != (1, gate.K, sg.N):
+                raise ValueError("shared must be (gate, up, down) of one expert")
+        self.router, self.gate, self.up, self.down, self.shared = router, gate, up, down, shared
+        self.E, self.f, self.d = gate.E, gate.N, gate.K
+        self._buffers = {}
+
+    def buffers(self, T: int, dtype: torch.dtype) -> dict:
+        key = (T, dtype)
+        if key not in self._buffers:
+            E, k, d, f, R = self.E, self.router.top_k, self.d, self.f, T * self.router.top_k
+
+            def new(shape, dt):
+                return torch.empty(shape, dtype=dt, device=self.gate.q.device)
+
+            b = dict(idx=new((T, k), torch.int32), w=new((T, k), torch.float32),
+                     off=new((E + 1,), torch.int32), perm=new((R,), torch.int32),
+                     pos=new((T, k), torch.int32), xq=new((T, d), torch.float8_e4m3fn),
+                     xs=new((T, blocks(d)), torch.float32),
+                     hq=new((R, f), torch.float8_e4m3fn),
+                     hs=new((R, blocks(f)), torch.float32), o=new((R, d), dtype), shared=None)
+            if self.shared is not None:
+                fs = self.shared[0].N
+                b.update(shq=new((T, fs), torch.float8_e4m3fn),
+                         shs=new((T, blocks(fs)), torch.float32), shared=new((T, d), dtype))
+            n = max(group_route_workspace_size(self.router, T), workspace_size(max(R, T)))
+            b["ws"] = torch.zeros(n, dtype=torch.uint8, device=self.gate.q.device)
+            self._buffers[key] = b
+        return self._buffers[key]
+
+    def forward(self, x: torch.Tensor, logits: torch.Tensor,
+                bias: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                stream=None) -> LayerOutput:
+        """y [T, d] of x [T, d] and its router logits [T, E]; y has x's type unless given."""
+        T = x.shape[0]
+        k = self.router.top_k
+        b = self.buffers(T, x.dtype)
+        if y is None:
+            y = torch.empty((T, self.d), dtype=x.dtype, device=x.device)
+        ws = b["ws"]
+        group_route(self.router, logits, bias, b["idx"], b["w"], b["off"], b["perm"], b["pos"], ws,
+                    stream)
+        quantize(x, b["xq"], b["xs"], stream)
+        swiglu(self.gate, self.up, b["xq"], b["xs"], b["hq"], b["hs"], ws, off=b["off"],
+               perm=b["perm"], top_k=k, stream=stream)
+        product(self.down, b["hq"], b["hs"], b["o"], ws, off=b["off"], stream=stream)
+        if self.shared is not None:
+            sg, su, sd = self.shared
+            swiglu(sg, su, b["xq"], b["xs"], b["shq"], b["shs"], ws, stream=stream)
+            product(sd, b["shq"], b["shs"], b["shared"], ws, stream=stream)
+        combine(b["o"], b["w"], b["pos"], y, shared=b["shared"], stream=stream)
+        return LayerOutput(y=y, **{n: b[n] for n in ("idx", "w", "off", "perm", "pos", "xq", "xs",
+                                                     "hq", "hs", "o", "shared")})

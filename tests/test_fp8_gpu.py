@@ -535,3 +535,102 @@ def test_operators_on_another_stream(fp8):
     assert torch.equal(here["y"], third["y"])
     for b in (here, there, third):
         assert fp8.check_device_error(b["ws"]) == 0
+
+
+# ---------------------------------------------------------------- the layer
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,E,k,G,g,d,f,fs", [(1, 32, 4, 4, 2, 512, 256, 256),
+                                              (37, 32, 4, 4, 2, 512, 272, 128),
+                                              (300, 4, 2, 1, 1, 400, 256, 0)])
+def test_layer_stage_by_stage(fp8, dt, T, E, k, G, g, d, f, fs):
+    """fp8.Layer's every stage against the reference on that stage's own inputs."""
+    rng = np.random.default_rng(T + E)
+    mats = [make_mat(fp8, rng, E, f, d), make_mat(fp8, rng, E, f, d), make_mat(fp8, rng, E, d, f)]
+    sh = [make_mat(fp8, rng, 1, fs, d), make_mat(fp8, rng, 1, fs, d),
+          make_mat(fp8, rng, 1, d, fs)] if fs else None
+    layer = fp8.Layer(fp8.make_router(E, k, G, g, s=2.5), *(m[2] for m in mats),
+                      shared=tuple(m[2] for m in sh) if fs else None)
+    x = dev(2 * rng.standard_normal((T, d)).astype(np.float32)).to(TYPES[dt])
+    logits = dev(rng.standard_normal((T, E)).astype(np.float32)).to(TYPES[dt])
+    bias = dev((0.1 * rng.standard_normal(E)).astype(np.float32))
+    out = layer.forward(x, logits, bias)
+    first = out.y.clone()
+    assert torch.equal(layer.forward(x, logits, bias).y, first)
+    assert fp8.check_device_error(layer.buffers(T, x.dtype)["ws"]) == 0
+    idx = out.idx.cpu().numpy()
+    ridx, rw, gap = ref.route(logits.float().cpu().numpy(), bias.cpu().numpy(), k, G, g, 0, True,
+                              True, 2.5)
+    assert np.array_equal(idx[gap > 1e-6], ridx[gap > 1e-6])
+    off, perm, pos = ref.permutation(idx, E)
+    assert np.array_equal(out.off.cpu().numpy(), off)
+    check_quantized(out.xq.view(torch.uint8), out.xs, x)
+    R = T * k
+
+    def codes_of(q, s):
+        return ref.dequantize(q.view(torch.uint8).cpu().numpy(), s.cpu().numpy())
+
+    xv = codes_of(out.xq, out.xs)
+    gu = [expected(xv, off, perm // k, m[0], m[1], R, f) for m in mats[:2]]
+    check_h(out.hq.view(torch.uint8), out.hs, gu[0][0], gu[0][1], gu[1][0], gu[1][1])
+    y, e = expected(codes_of(out.hq, out.hs), off, np.arange(R), mats[2][0], mats[2][1], R, d)
+    check_out(out.o, y, e, dt)
+    o = out.o.double().cpu().numpy()
+    w = out.w.double().cpu().numpy()
+    terms = w[..., None] * o[pos]
+    base = 0.0
+    if fs:
+        b = layer.buffers(T, x.dtype)
+        one = np.array([0, T])
+        gu = [expected(xv, one, np.arange(T), m[0], m[1], T, fs) for m in sh[:2]]
+        check_h(b["shq"].view(torch.uint8), b["shs"], gu[0][0], gu[0][1], gu[1][0], gu[1][1])
+        y, e = expected(codes_of(b["shq"], b["shs"]), one, np.arange(T), sh[2][0], sh[2][1], T, d)
+        check_out(out.shared, y, e, dt)
+        base = out.shared.double().cpu().numpy()
+    y = terms.sum(1) + base
+    check_out(first, y, (np.abs(terms).sum(1) + np.abs(base)) * (k + 2) * ref.U32, dt)
+
+
+def test_layer_example(gpu):
+    """The example's layer stays near the float32 one: each of the three quantisations
+    errs by at most 2^-4 of a value, independently over the hundreds that enter an
+    output, so the whole stays far below 0.2 of a row's largest."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "fp8_layer.py")
+    spec = importlib.util.spec_from_file_location("fp8_layer_example", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    for n in (1, 33, 512):
+        err, _ = example.run(n)
+        assert err < 0.2, err
+
+
+def test_layer_refusals(fp8):
+    rng = np.random.default_rng(1)
+    gate, down = make_mat(fp8, rng, 4, 64, 128)[2], make_mat(fp8, rng, 4, 128, 64)[2]
+    wrong = make_mat(fp8, rng, 4, 64, 112)[2]
+    with pytest.raises(ValueError):
+        fp8.Layer(fp8.make_router(4, 2), gate, wrong, down)
+    with pytest.raises(ValueError):
+        fp8.Layer(fp8.make_router(8, 2), gate, gate, down)
+    with pytest.raises(ValueError):
+        fp8.Layer(fp8.make_router(4, 2), gate, gate, down, shared=(gate, gate, down))
+    x = torch.zeros((3, 128), device="cuda")
+    out = torch.zeros((6, 128), device="cuda")
+    with pytest.raises(fp8.MoeError):  # more rows asked for than there are activations
+        fp8.product(down, torch.zeros((3, 64), dtype=torch.uint8, device="cuda"),
+                    torch.zeros((3, 1), device="cuda"), out, workspace(fp8, 6),
+                    off=torch.zeros(5, dtype=torch.int32, device="cuda"))
+    with pytest.raises(fp8.MoeError):
+        fp8.product(down, torch.zeros((3, 64), dtype=torch.uint8, device="cuda"),
+                    torch.zeros((3, 1), device="cuda"), out[:3],
+                    torch.zeros(256, dtype=torch.uint8, device="cuda"),
+                    off=torch.zeros(5, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        fp8.quantize(x.double(), x, x)
+    with pytest.raises(ValueError):
+        fp8.quantize(x.t(), x, x)
+    with pytest.raises(ValueError):
+        fp8.quantize(x[:1].expand(3, 128), x, x)
