@@ -147,9 +147,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         uint8_t *buf = tsm + s * kStage, *dst = buf + kXBytes;
         bar_expect(&full[s], bytes);
         for (int h = 0; h < nb; ++h)
-          tma_w<1>(dst + h * kWBytes, &maps.w[SWIGLU ? h : 0], kb * 128,
+          tma_w(dst + h * kWBytes, &maps.w[SWIGLU ? h : 0], kb * 128,
                    (SWIGLU ? t.nt : t.nt * NB + h) * 128, t.e, &full[s]);
-        if (!gather) tma_x<1>(buf, &maps.x, kb * 128, t.row0, &full[s]);
+        if (!gather) tma_x(buf, &maps.x, kb * 128, t.row0, &full[s]);
       }
     }
     // the stages still in use: leave with no copy in flight
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   } else if (warp == 1) {
     // ============================ MMA issuer
     Ring st, acc;
-    const uint32_t idesc = idesc_for<1>(MT);
+    const uint32_t idesc = idesc_for(MT);
     while (!guard.aborted() && walk.take(seg)) {
       const int nb = blocks_of(fp8_tile<MT>(a, rt, seg.tile));
       for (int kb = seg.kb0; kb < seg.kb1; ++kb, st.next(n_stages), acc.next(kAccs)) {
@@ -171,14 +171,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         const uint32_t buf = s32(tsm + st.i * kStage);
         const uint64_t xd = sw128_desc(buf), wd = sw128_desc(buf + kXBytes);
         const uint32_t d = tmem + acc.i * NB * MT;
-        tc_mma_block<1>(d, wd, xd, idesc);
-        if (NB == 2 && nb == 2) tc_mma_block<1>(d + MT, wd + (kWBytes >> 4), xd, idesc);
-        tc_commit<1>(&empty[st.i]);
-        tc_commit<1>(&d_full[acc.i]);
+        tc_mma_block(d, wd, xd, idesc);
+        if (NB == 2 && nb == 2) tc_mma_block(d + MT, wd + (kWBytes >> 4), xd, idesc);
+        tc_commit(&empty[st.i]);
+        tc_commit(&d_full[acc.i]);
       }
     }
     if (guard.aborted()) {  // else the epilogue has waited for every MMA
-      tc_commit<1>(drain);
+      tc_commit(drain);
       bar_wait_for(drain, 0);
     }
   } else if (warp == 2) {

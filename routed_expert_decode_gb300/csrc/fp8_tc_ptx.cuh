@@ -71,51 +71,21 @@ __device__ __forceinline__ void bar_wait(uint64_t *b, uint32_t parity, const Gua
   if (!*g.abort_flag) atomicOr(g.err, kErrTimeout);
   *g.abort_flag = 1;
 }
-// arrive on the same barrier of the pair's first CTA
-__device__ __forceinline__ void bar_arrive_first(uint64_t *b) {
-  asm volatile(
-      "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, 0;\n"
-      " mbarrier.arrive.shared::cluster.b64 _, [r];\n}\n" ::"r"(s32(b))
-      : "memory");
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
-}
-// Tensor copies.  In a pair (CG = 2) both CTAs' copies complete on the first CTA's
-// barrier: the address of a shared-memory object of this CTA with the bit that
-// tells the pair's CTAs apart cleared is the object's in the first.
-constexpr uint32_t kFirstCta = 0xFEFFFFFFu;
-template <int CG>
 __device__ __forceinline__ void tma_w(void *dst, const CUtensorMap *map, int k, int n, int e,
                                       uint64_t *bar) {
-  if (CG == 2)
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(s32(dst)),
-        "l"(map), "r"(k), "r"(n), "r"(e), "r"(s32(bar) & kFirstCta)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(s32(dst)),
-        "l"(map), "r"(k), "r"(n), "r"(e), "r"(s32(bar))
-        : "memory");
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(s32(dst)),
+      "l"(map), "r"(k), "r"(n), "r"(e), "r"(s32(bar))
+      : "memory");
 }
-template <int CG>
 __device__ __forceinline__ void tma_x(void *dst, const CUtensorMap *map, int k, int row,
                                       uint64_t *bar) {
-  if (CG == 2)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(s32(dst)),
-        "l"(map), "r"(k), "r"(row), "r"(s32(bar) & kFirstCta)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(s32(dst)),
-        "l"(map), "r"(k), "r"(row), "r"(s32(bar))
-        : "memory");
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(s32(dst)),
+      "l"(map), "r"(k), "r"(row), "r"(s32(bar))
+      : "memory");
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -127,6 +97,10 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes, b
       " @p cp.async.cg.shared.global [%0], [%1], 16, %2;\n}\n" ::"r"(dst),
       "l"(src), "r"(bytes), "r"((int)go)
       : "memory");
+}
+// 4 bytes global -> shared
+__device__ __forceinline__ void cp4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 // this thread arrives on b once its copies so far have landed
 __device__ __forceinline__ void cp_arrive(uint64_t *b) {
@@ -144,43 +118,27 @@ __device__ __forceinline__ void tc_fence_after() {
 // The products of one block of 128 along K, D = A B^T from zero: four MMAs of K = 32,
 // 32 bytes apart along the operands' rows (2 in the descriptors' units).  Called by
 // a whole converged warp with uniform operands; one lane issues.
-#define MOE_MMA4(G)                                                                  \
-  asm volatile(                                                                      \
-      "{\n .reg .pred e, f, t;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"                \
-      " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"              \
-      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"              \
-      " setp.ne.b32 f, 0, 0;\n setp.eq.b32 t, 0, 0;\n elect.sync _|e, 0xffffffff;\n" \
-      " @e tcgen05.mma.cta_group::" G ".kind::f8f6f4 [%0], %1, %2, %3, f;\n"         \
-      " @e tcgen05.mma.cta_group::" G ".kind::f8f6f4 [%0], a1, b1, %3, t;\n"         \
-      " @e tcgen05.mma.cta_group::" G ".kind::f8f6f4 [%0], a2, b2, %3, t;\n"         \
-      " @e tcgen05.mma.cta_group::" G ".kind::f8f6f4 [%0], a3, b3, %3, t;\n}\n" ::   \
-          "r"(d_tmem),                                                               \
-      "l"(a_desc), "l"(b_desc), "r"(idesc)                                           \
-      : "memory")
-template <int CG>
 __device__ __forceinline__ void tc_mma_block(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                              uint32_t idesc) {
-  if (CG == 2)
-    MOE_MMA4("2");
-  else
-    MOE_MMA4("1");
+  asm volatile(
+      "{\n .reg .pred e, f, t;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+      " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
+      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+      " setp.ne.b32 f, 0, 0;\n setp.eq.b32 t, 0, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, t;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc)
+      : "memory");
 }
-#undef MOE_MMA4
-// arrive on b (in a pair: on both CTAs' b) when the MMAs so far are done
-template <int CG>
+// arrive on b when the MMAs so far are done
 __device__ __forceinline__ void tc_commit(uint64_t *bar) {
-  if (CG == 2)
-    asm volatile(
-        "{\n .reg .pred e;\n .reg .b16 m;\n elect.sync _|e, 0xffffffff;\n mov.b16 m, 3;\n"
-        " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
-        ".multicast::cluster.b64 [%0], m;\n}\n" ::"r"(s32(bar))
-        : "memory");
-  else
-    asm volatile(
-        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::
-            "r"(s32(bar))
-        : "memory");
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          s32(bar))
+      : "memory");
 }
 // 32 consecutive fp32 columns of this warp's 32 TMEM lanes, no wait
 __device__ __forceinline__ void tc_ld32(uint32_t taddr, float (&v)[32]) {
@@ -217,11 +175,9 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
   return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-// instruction descriptor: D f32, A and B e4m3, both K-major, N >> 3 at bit 17, M >> 4
-// at bit 24 (M = 128 a CTA)
-template <int CG>
+// instruction descriptor: D f32, A and B e4m3, both K-major, N >> 3 at bit 17, M = 128
 __device__ __forceinline__ uint32_t idesc_for(uint32_t n) {
-  return (1u << 4) | ((n >> 3) << 17) | (8u * CG << 24);
+  return (1u << 4) | ((n >> 3) << 17) | (8u << 24);
 }
 
 // a place in a ring of n stages: its index and the parity of its current use
