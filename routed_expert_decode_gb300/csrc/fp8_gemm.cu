@@ -168,8 +168,9 @@ cudaError_t launch_fp8_gemm(const Fp8Call &c) {
   a.sync = (uint32_t *)(c.ws + 256) + kFp8TileSync;
   a.part = (float *)(c.ws + MOE_WS_FIXED_BYTES);
   if (fp8_tc_ok(a))
-    return a.R <= kFp8FewRows * a.E ? launch_fp8_few(a, c.swiglu, c.stream)
-                                    : launch_fp8_tc(a, c.swiglu, c.stream);
+    return a.R <= (c.swiglu ? kFp8FewSwiglu : kFp8FewProduct64) * a.E
+               ? launch_fp8_few(a, c.swiglu, c.stream)
+               : launch_fp8_tc(a, c.swiglu, c.stream);
   return c.swiglu ? run_core<true>(a, c.stream) : run_core<false>(a, c.stream);
 }
 

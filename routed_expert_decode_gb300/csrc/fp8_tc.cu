@@ -1,38 +1,41 @@
 // fp8_tc.cu -- routed and dense products over block-scaled e4m3 operands on the
-// 5th-generation tensor cores.
+// 5th-generation tensor cores, for experts with many rows: bound by arithmetic.
 //
-// A tile is a run of activation rows of one expert by NH blocks of 128 weight rows
-// (NH = 2: 256 columns of the product, or the gate and up rows of one block of 128
-// features).  Per block of 128 along K, tcgen05.mma kind::f8f6f4 (M = 128 rows a
-// CTA, K = 32 four times) forms the unscaled products in one of two TMEM
-// accumulators, and the epilogue warps add them, times scale_x * scale_w, to fp32
-// sums in registers: the scales change every 128 K, so each accumulator is read
-// once per block.  The activation rows sit on the MMA's M side, so that an
-// epilogue thread owns one row: its scale product is one scalar per block and
-// matrix, a pair of columns costs one packed FMA, and a row's quantisation block
-// after SwiGLU is a maximum over two threads' registers.
+// A tile is 128 activation rows of one expert by two blocks of 128 weight rows (256
+// columns of the product, or the gate and up rows of one block of 128 features).
+// Per block of 128 along K, tcgen05.mma kind::f8f6f4 (M = 128, N = 256, K = 32 four
+// times) forms the unscaled products in one of two TMEM accumulators, and the
+// epilogue warps add them, times scale_x * scale_w, to fp32 sums in registers: the
+// scales change every 128 K, so each accumulator is read once per block.  The
+// activation rows sit on the MMA's M side, so that an epilogue thread owns one row:
+// its scale product is one scalar per block and matrix, a pair of columns costs one
+// packed FMA, and a row's quantisation block after SwiGLU is a maximum over two
+// threads' registers.
 //
-// Dead rows (tiles of a few rows) cost MMA time but no bytes: at M = 128 the
-// tensor cores consume a block's 32 KB of weights in ~512 clocks, HBM delivers an
-// SM's share of them in ~1400, so one layout serves decode and prefill.
+// What bounds it: that epilogue.  Its 32768 FMAs and 128 KB of TMEM reads a block
+// take ~340 clocks of the SM's four schedulers against the MMA's 512, but the chain MMA
+// -> loads -> FMAs -> release -> MMA, with two accumulators to hide it in, comes to ~950.
+// 16384 rows of gate/up (d 6144, f 2048, 16 experts): 430 us, 1.92 PFLOP/s; 4000 x
+// 4096 x 6144 dense: 115 us, 1.75 PFLOP/s.  Without the epilogue the same tiles take 332 and
+// 75 us, of which the second is L2's bandwidth (48 KB a block and SM, 16 TB/s).
+// Measured and not kept: pairs of CTAs on 256 rows (cta_group::2, which halves an SM's
+// weight bytes: 504 and 122 against 476 and 119 us -- the other CTA's arrivals lengthen
+// the chain); accumulators of one weight block each, four in flight (494 and 131:
+// the MMA's issue and waits double); TMA's gather of four rows for the routed
+// activations (78 clocks a request, 2500 a tile of 128 rows and block).
+//
 // Routed activation rows are copied by 16-byte cp.async through perm into the
-// swizzled layout, so no permuted copy of the activations is written (TMA's
-// gather of 4 rows a request took ~78 clocks a request, 2500 a tile of 128 rows);
-// rows in order come by one TMA box.
+// swizzled layout, so no permuted copy of the activations is written; rows in
+// order come by one TMA box.  The scales follow by 4-byte cp.async: loads of them in
+// the epilogue took 9 % of the kernel however far ahead they were issued.
 //
-// Many rows (CG = 2): a pair of CTAs works on 256 rows with cta_group::2, each SM
-// holding its own 128 rows and one of the two weight blocks, so that an SM takes in
-// 32 KB a block instead of 48 (an SM's share of L2's bandwidth is ~64 bytes a
-// clock, 768 clocks for 48 KB, against the MMA's 512).
+// Warps: 0 weights and scales, 1 TMEM owner and MMA issuer, 2 and 3 routed activations,
+// 4..11 epilogue (warp w reads TMEM lanes 32*(w%4).., columns by half).
 //
-// Warps: 0 weights producer, 1 TMEM owner and MMA issuer (in the pair's second
-// CTA: it passes on that its activations have landed), 2 and 3 activations, 4..11
-// epilogue (warp w reads TMEM lanes 32*(w%4).., columns by half).
-//
-// Work goes out over one CTA (pair) per SM (pair): whole tiles in rounds, and the
-// tiles of the last, partial round cut along K into equal shares where whole tiles
-// would leave too many SMs idle (first in every CTA's order).  The shares of a
-// tile meet in the workspace: each CTA writes its fp32 sums, the last one to
+// Work goes out over one CTA per SM: whole tiles in rounds, and the tiles of the last,
+// partial round cut along K into equal shares unless nearly every SM would have one
+// (first in every CTA's order; 16384 rows of gate/up: 476 us split, 484 whole).  The
+// shares of a tile meet in the workspace: each CTA writes its fp32 sums, the last one to
 // arrive adds all of them in ascending K, so the result does not depend on the
 // order of arrival.
 #include <string.h>
@@ -43,20 +46,22 @@ namespace moe {
 namespace {
 
 constexpr int kTcThreads = 12 * 32;
+constexpr uint32_t kTcStages = 4;  // of the operand ring, at most
 constexpr int kEpiWarp0 = 4;
 constexpr int kM = 128;  // rows of a tile
-// Scales of the blocks of K in flight.  A block's are written when the MMA four
-// blocks (a ring of stages) earlier is done, which was issued when the epilogue had
-// read the block two before that: a slot of the seventh block back is free.
+// Scales of the blocks of K in flight.  A block's are written when the MMA a ring of
+// stages earlier is done, which was issued when the epilogue had read the block two
+// before that: the slot of the block two further back is free.
 constexpr uint32_t kScaleSlots = 8;
+static_assert(kTcStages + 3 <= kScaleSlots, "a slot's last reader is done");
 constexpr uint32_t kABytes = kM * 128, kStage = kABytes + 2 * kWBytes;
-// registers per thread after the split: 128 * 56 + 256 * 224 = 384 * 168, the launch's
-constexpr int kRegsRole = 56, kRegsEpi = 224;
+// registers per thread after the split: 128 * 72 + 256 * 216 = 384 * 168, the launch's;
+// with 56 the activations' row numbers spill (437 against 429 us)
+constexpr int kRegsRole = 72, kRegsEpi = 216;
 
-
-// A row's product over one segment leaves up to 128 fp32 sums in each of its two
-// epilogue threads: acc[0..31] and acc[32..63] are pairs of columns -- of the
-// gate and the up block (SwiGLU), or of a block's two halves.
+// A row's product over one segment leaves 128 fp32 sums in each of its two epilogue
+// threads: acc[0..31] and acc[32..63] are pairs of columns -- of the gate and the
+// up block (SwiGLU), or of a block's two halves.
 template <bool SWIGLU>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_fp8_tc(const Fp8Args a, const __grid_constant__ Fp8Maps maps, const uint32_t n_stages,
@@ -188,7 +193,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     } else if (warp >= 2 && gather) {
       // ============================ activations through perm: in instruction j of
-      // MT / 8, warp w copies rows 8j + 4w .. + 3, eight lanes a row of 128 codes
+      // 16, warp w copies rows 8j + 4w .. + 3, eight lanes a row of 128 codes
       constexpr int kJ = kM / 8;
       const int r0 = 4 * (warp - 2) + lane / 8, chunk = lane & 7;
       Ring st;
@@ -426,8 +431,7 @@ template <bool SWIGLU>
 cudaError_t run_tc(Fp8Args &a, cudaStream_t stream) {
   const int sms = fp8_ctas();
   fp8_set_tiles(a, SWIGLU ? a.nbn : (a.nbn + 1) / 2, sms);
-  const uint32_t quarters = ((a.R < 128 ? a.R : 128) + 31) / 32;
-  a.part_stride = (size_t)quarters * 8192;
+  a.part_stride = fp8_part_bytes(a.R) / 4;
   Fp8Maps maps;
   memset(&maps, 0, sizeof maps);
   if (!byte_map(&maps.x, a.xq, a.K, a.n_x, 1, 2, kM) ||
@@ -441,7 +445,7 @@ cudaError_t run_tc(Fp8Args &a, cudaStream_t stream) {
   auto kern = k_fp8_tc<SWIGLU>;
   const size_t rest = 1024 + 512 + 2048 + 4 * kScaleSlots * (kM + 2) + fp8_tiles_smem(a.E);
   int ns = (int)((kSmemLimit - rest) / kStage);
-  if (ns > kMaxStages) ns = kMaxStages;
+  if (ns > (int)kTcStages) ns = kTcStages;
   const size_t smem = rest + ns * (size_t)kStage;
   static int set[kMaxDevices];
   const cudaError_t e = allow_smem(kern, smem, set);
@@ -457,11 +461,17 @@ bool fp8_tc_ok(const Fp8Args &a) {
   return a.K % 16 == 0 && a16(a.xq) && a16(a.wq[0]) && a16(a.wq[1]) && encode_fn() != nullptr;
 }
 
-size_t fp8_tc_ws(uint32_t rows) {
-  // two parts a CTA, each 128 sums of fp32 in 64 threads per 32 rows
-  const size_t quarters = ((rows < 128 ? rows : 128) + 31) / 32;
-  return (size_t)fp8_ctas() * 2 * quarters * 32768;
+size_t fp8_part_bytes(uint32_t rows) {
+  // 256 columns of fp32 for each row of the largest tile that a call of so many rows
+  // can take: the few-row kernels' 32 or 64, the many-row kernel's 128 in runs of 32
+  const uint32_t r = rows <= kFp8FewProduct32 ? 32
+                     : rows <= 64             ? 64
+                     : rows < 128             ? (rows + 31) / 32 * 32
+                                              : 128;
+  return (size_t)r * 1024;
 }
+
+size_t fp8_tc_ws(uint32_t rows) { return (size_t)fp8_ctas() * 2 * fp8_part_bytes(rows); }
 
 cudaError_t launch_fp8_tc(Fp8Args &a, bool swiglu, cudaStream_t stream) {
   return swiglu ? run_tc<true>(a, stream) : run_tc<false>(a, stream);

@@ -427,6 +427,7 @@ cudaError_t run_few(Fp8Args &a, cudaStream_t stream) {
   const int sms = fp8_ctas();
   fp8_set_tiles(a, SWIGLU ? a.nbn : (a.nbn + NB - 1) / NB, sms);
   a.part_stride = (size_t)MT * 256;
+  if (a.part_stride * 4 > fp8_part_bytes(a.R)) return cudaErrorInvalidValue;
   Fp8Maps maps;
   memset(&maps, 0, sizeof maps);
   if (!byte_map(&maps.x, a.xq, a.K, a.n_x, 1, 2, MT) ||
@@ -455,8 +456,8 @@ cudaError_t run_few(Fp8Args &a, cudaStream_t stream) {
 
 cudaError_t launch_fp8_few(Fp8Args &a, bool swiglu, cudaStream_t stream) {
   const uint64_t R = a.R, E = a.E;
-  if (R > 32 * E) return swiglu ? run_few<true, 64, 2>(a, stream) : run_few<false, 64, 2>(a, stream);
   if (swiglu) return run_few<true, 32, 2>(a, stream);
+  if (R > kFp8FewProduct32 * E) return run_few<false, 64, 2>(a, stream);
   // At most this many pairs of weight blocks have rows.  Few rounds of tiles go out
   // more evenly one block a tile (one token's down projection, 192 pairs: 22.0
   // against 23.1 us); with many rounds a pair shares a tile's fixed work.

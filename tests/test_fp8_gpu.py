@@ -313,6 +313,10 @@ PRODUCT_CASES = [
     (64, 40, 6, 256, 384, (3, 4, 5, 39)),
     (300, 3, 2, 512, 640, ()),
     (260, 1, 1, 2064, 520, ()),
+    # 25 to 64 rows of one expert, whose tiles are split along K
+    (25, 1, 1, 2064, 200, ()),
+    (55, 1, 1, 1040, 300, ()),
+    (128, 1, 1, 1552, 144, ()),
     (2, 1024, 8, 128, 128, ()),
     # a reduction length that tensor copies cannot take
     (5, 3, 2, 100, 130, ()),

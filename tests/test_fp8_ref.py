@@ -165,6 +165,16 @@ def test_product_refusals(fp8):
     assert call(swiglu=True, ld=0) == 1
 
 
+def test_workspace_grows_with_the_tiles(fp8):
+    """A split tile's share holds 256 columns of fp32 for each row of its tile, two
+    shares a CTA: the sizes behind the fixed head step with the tile rows."""
+    ctas = (fp8.workspace_size(64) - fp8.workspace_size(1)) // (2 * 32 * 1024)
+    assert ctas >= 1
+    for rows, tile in ((1, 32), (24, 32), (25, 64), (64, 64), (65, 96), (96, 96), (97, 128),
+                       (128, 128), (10 ** 6, 128)):
+        assert fp8.workspace_size(rows) - fp8.workspace_size(1) == 2 * ctas * 1024 * (tile - 32)
+
+
 def test_python_refusals(fp8):
     import torch
 
