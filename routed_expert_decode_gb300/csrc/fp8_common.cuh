@@ -20,10 +20,9 @@ __host__ __device__ constexpr uint32_t fp8_blocks(uint32_t n) {
 
 // words of the workspace's counter area (moe.h) used by these operators, clear
 // of the layer's: zero between calls
-constexpr uint32_t kFp8RouteSync = 2064;     // [2]: CTAs in, CTAs out of the permutation's barrier
 constexpr uint32_t kFp8TileSync = 2080;      // [kFp8MaxCtas * 4]: parts of a split tile done
 constexpr uint32_t kFp8MaxCtas = 256;
-static_assert(kQueueTcDown + 2 <= kFp8RouteSync &&
+static_assert(kQueueTcDown + 2 <= kFp8TileSync &&
                   kFp8TileSync + kFp8MaxCtas * 4 <= MOE_SYNC_BYTES / 4 - 2,
               "counters overlap the layer's");
 

@@ -1,5 +1,5 @@
 // group_route.cu -- group-limited top-k routing and the stable permutation of
-// the (token, slot) rows by expert, in one kernel.
+// the (token, slot) rows by expert.
 //
 // Many tokens: a warp selects for a token, and a second kernel permutes.
 // The token's logits go to shared memory, where one rolled loop turns them into
@@ -13,12 +13,13 @@
 // that holds it wins); the winner goes on to its second-best, and looks through its
 // registers again only when that is used up.
 //
-// Permutation: up to 64 CTAs, each with a run of the tokens.  A CTA counts its rows
-// per expert, and after a grid-wide barrier adds up the counts of the CTAs before it
-// and of the experts before each expert: where its rows of each expert start.  A token
-// picks an expert at most once, so the rank of row (t, j) among its expert's rows of
-// a run of tokens is a population count over the expert's token mask below bit t.
-// No order of atomics enters the result.
+// Permutation: up to 64 CTAs, each with a run of the tokens.  The selecting warps count
+// the picks of each run per expert (in counters that a kernel before them clears), and
+// a CTA adds up the counts of the runs before its own and of the experts before
+// each expert: where its rows of each expert start.  A token picks an expert at
+// most once, so the rank of row (t, j) among its expert's rows of a run of tokens is a
+// population count over the expert's token mask below bit t.  No order of atomics
+// enters the result, and no CTA waits for another.
 //
 // Few rows: one CTA, a thread for each expert of a token: an expert's place is the
 // number of kept ones before it, so there are no rounds; rows are ranked by
@@ -26,9 +27,10 @@
 //
 // What bounds it: for many tokens the selection's issue slots (256 experts, top 8:
 // ~1100 warp instructions a token; the logits are read once) and the fixed steps of
-// the permutation (~7 us: launch, barrier, counts); for few tokens the chain of a
-// launch and its dependent steps.  256 experts in 8 groups, 4 kept, top 8: 8192 tokens
-// 22 us, 256 tokens 11, 32 tokens 7.3, one 5.1.
+// the permutation (two launches and two passes over its picks, ~5 us); for few tokens
+// the chain of a launch and its dependent steps.  256 experts in 8 groups, 4 kept, top
+// 8: 8192 tokens 21.0 us, 256 tokens 9.7, 32 tokens 7.5, one 5.1.  A permutation that
+// counted by itself behind a grid-wide barrier: 22.6 and 11.2 us for 8192 and 256.
 #include <float.h>
 
 #include "fp8_common.cuh"
@@ -47,8 +49,6 @@ constexpr int kPlaceThreads = 1024;
 constexpr uint32_t kPlaceCtas = 64;
 constexpr uint32_t kPlaceWords = 4;                  // mask words of an expert
 constexpr uint32_t kPlaceTokens = 32 * kPlaceWords;  // tokens ranked at a time
-constexpr long long kGrWaitCycles = 4000000000ll;
-constexpr int kGrSpinIters = 1 << 26;
 
 struct GrArgs {
   moe_router r;
@@ -60,7 +60,15 @@ struct GrArgs {
   int32_t *idx;
   float *w;
   int32_t *off, *perm, *pos;
+  int32_t *hist;          // [runs][E] picks of each run's tokens, or null (one run)
+  uint32_t per, per_inv;  // tokens of a run, floor((2^32 - 1) / per)
 };
+
+// v / d with inv = floor((2^32 - 1) / d): the product's high word is at most one short
+__device__ __forceinline__ uint32_t quot(uint32_t v, uint32_t d, uint32_t inv) {
+  const uint32_t q = __umulhi(v, inv);
+  return v - q * d >= d ? q + 1 : q;
+}
 
 // The arguments into the constant cache before the wait for earlier work: a
 // launch's are always cold, and the first uses come one after another.
@@ -68,7 +76,7 @@ __device__ __forceinline__ void gr_warm(const GrArgs &a) {
   asm volatile("" ::"r"(a.r.n_expert), "r"(a.r.top_k), "r"(a.r.n_group), "r"(a.r.topk_group),
                "r"(a.r.score), "r"(a.r.group_score), "r"(a.r.renorm), "f"(a.r.s), "l"(a.logits),
                "r"(a.dt), "l"(a.ld), "l"(a.bias), "r"(a.T), "r"(a.gsize), "l"(a.idx), "l"(a.w),
-               "l"(a.off), "l"(a.perm), "l"(a.pos));
+               "l"(a.off), "l"(a.perm), "l"(a.pos), "l"(a.hist), "r"(a.per), "r"(a.per_inv));
 }
 
 // order-preserving map of a float (never NaN) to an unsigned above 0; -0 as +0
@@ -268,6 +276,7 @@ __device__ __forceinline__ void route_token(const GrArgs &a, uint32_t t, int lan
   if (slot) {
     a.idx[(size_t)t * k + lane] = mine;
     a.w[(size_t)t * k + lane] = w;
+    if (a.hist) atomicAdd(a.hist + (size_t)quot(t, a.per, a.per_inv) * E + mine, 1);
   }
 }
 
@@ -282,50 +291,24 @@ __global__ void __launch_bounds__(kGrWarps * 32) k_group_route(const GrArgs a) {
   if (t < a.T) route_token<NPER>(a, t, threadIdx.x & 31, sc[warp]);
 }
 
-// grid-wide barrier on sync[0] (CTAs in) and sync[1] (CTAs out; the last one
-// zeroes both).  The launch is cooperative, so every CTA is resident; the wait
-// is bounded all the same.  False: it gave up.
-__device__ bool grid_barrier(uint32_t *sync, uint32_t n, uint32_t *err) {
-  __shared__ int ok;
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    ok = 1;
-    atomicAdd(sync, 1u);
-    const long long t0 = clock64();
-    volatile uint32_t *in = sync;
-    int i = 0;
-    while (*in < n) {
-      if (++i > kGrSpinIters || clock64() - t0 > kGrWaitCycles) {
-        atomicOr(err, kErrTimeout);
-        ok = 0;
-        break;
-      }
-    }
-    __threadfence();
-    if (ok && atomicAdd(sync + 1, 1u) == n - 1) {
-      atomicExch(sync, 0u);
-      atomicExch(sync + 1, 0u);
-    }
-  }
-  __syncthreads();
-  return ok != 0;
+__global__ void __launch_bounds__(1024) k_group_clear(int32_t *hist, uint32_t n) {
+  pdl_trigger();
+  pdl_wait();
+  for (uint32_t i = blockIdx.x * 1024 + threadIdx.x; i < n; i += gridDim.x * 1024) hist[i] = 0;
 }
 
 struct PlaceArgs {
   const int32_t *idx;
   uint32_t T, per, k, k_inv, E;  // per: tokens of a CTA; k_inv = floor((2^32 - 1) / k)
   int32_t *off, *perm, *pos;
-  int32_t *hist;   // [CTAs][E]: rows of each CTA's tokens per expert
-  uint32_t *sync;  // [2]
-  uint32_t *err;
+  const int32_t *hist;  // [CTAs][E]: rows of each CTA's tokens per expert
 };
 
 // off, perm and pos: CTA c places the rows of tokens [c*per, (c+1)*per)
 __global__ void __launch_bounds__(kPlaceThreads) k_group_place(const PlaceArgs a) {
   pdl_trigger();
   asm volatile("" ::"l"(a.idx), "r"(a.T), "r"(a.per), "r"(a.k), "r"(a.k_inv), "r"(a.E), "l"(a.off),
-               "l"(a.perm), "l"(a.pos), "l"(a.hist), "l"(a.sync));
+               "l"(a.perm), "l"(a.pos), "l"(a.hist));
   extern __shared__ __align__(16) uint8_t psm[];
   const uint32_t E = a.E, k = a.k, c = blockIdx.x;
   uint32_t *mask = (uint32_t *)psm;             // [E][words]
@@ -342,20 +325,14 @@ __global__ void __launch_bounds__(kPlaceThreads) k_group_place(const PlaceArgs a
     const int32_t *p = a.idx + (size_t)x * k;
     for (uint32_t i = tid; i < n; i += kPlaceThreads) use(p[i], i);
   };
-  auto token_of = [&](uint32_t i) {  // i / k
-    const uint32_t q = __umulhi(i, a.k_inv);
-    return i - q * k >= k ? q + 1 : q;
-  };
-  each(t0, t1, [&](int e, uint32_t) { atomicAdd(&count[e], 1); });
-  __syncthreads();
+  auto token_of = [&](uint32_t i) { return quot(i, k, a.k_inv); };
   int all = 0, ahead = 0;  // thread e: rows of expert e, and those of earlier CTAs
   if (gridDim.x == 1) {
+    each(t0, t1, [&](int e, uint32_t) { atomicAdd(&count[e], 1); });
+    __syncthreads();
     if ((uint32_t)tid < E) all = count[tid];
   } else {
-    for (uint32_t e = tid; e < E; e += kPlaceThreads)
-      __stcg(a.hist + (size_t)c * E + e, count[e]);
-    if (!grid_barrier(a.sync, gridDim.x, a.err)) return;
-    // kPlaceThreads / E threads an expert share the CTAs' counts
+    // kPlaceThreads / E threads an expert share the runs' counts
     int *part = (int *)mask;  // [2][E], free until the ranking
     for (uint32_t e = tid; e < 2 * E; e += kPlaceThreads) part[e] = 0;
     __syncthreads();
@@ -614,35 +591,40 @@ cudaError_t launch_group_route(const moe_router &r, const void *logits, int dt, 
   a.off = off;
   a.perm = perm;
   a.pos = pos;
+  a.hist = nullptr;
+  a.per = a.per_inv = 0;
   if (T <= kGrFewTokens) {
     const uint32_t team = (r.n_expert + 31) / 32 * 32;
     const uint32_t teams = T < kGrFewThreads / team ? (T ? T : 1) : kGrFewThreads / team;
     return launch_k(k_group_few, 1, team * teams, 0, stream, true, a, team);
   }
-  cudaError_t e = launch_select(a, stream);
+  // a run of 128 tokens a CTA of the permutation, more once there are 64
+  uint32_t grid = (T + kPlaceTokens - 1) / kPlaceTokens;
+  if (grid > kPlaceCtas) grid = kPlaceCtas;
+  a.per = (T + grid - 1) / grid;
+  a.per_inv = 0xffffffffu / a.per;
+  cudaError_t e = cudaSuccess;
+  if (grid > 1) {
+    a.hist = (int32_t *)((uint8_t *)ws + MOE_WS_FIXED_BYTES);
+    const uint32_t n = grid * r.n_expert;
+    e = launch_k(k_group_clear, (n + 4095) / 4096, 1024, 0, stream, true, a.hist, n);
+    if (e != cudaSuccess) return e;
+  }
+  e = launch_select(a, stream);
   if (e != cudaSuccess) return e;
   PlaceArgs p;
   p.idx = idx;
   p.T = T;
+  p.per = a.per;
   p.k = r.top_k;
   p.k_inv = 0xffffffffu / r.top_k;
   p.E = r.n_expert;
   p.off = off;
   p.perm = perm;
   p.pos = pos;
-  p.hist = (int32_t *)((uint8_t *)ws + MOE_WS_FIXED_BYTES);
-  p.sync = (uint32_t *)((uint8_t *)ws + 256) + kFp8RouteSync;
-  p.err = (uint32_t *)ws;
-  // a run of 128 tokens a CTA (one CTA needs no barrier), more once there are 64
-  uint32_t grid = (T + kPlaceTokens - 1) / kPlaceTokens;
-  const uint32_t most = (uint32_t)fp8_ctas() < kPlaceCtas ? (uint32_t)fp8_ctas() : kPlaceCtas;
-  if (grid > most) grid = most;
-  p.per = (T + grid - 1) / grid;
+  p.hist = a.hist;
   const size_t smem = (size_t)p.E * (kPlaceWords + 1) * 4;
-  if (grid == 1) return launch_k(k_group_place, 1, kPlaceThreads, smem, stream, true, p);
-  void *args[] = {&p};
-  return cudaLaunchCooperativeKernel((const void *)k_group_place, dim3(grid), dim3(kPlaceThreads),
-                                     args, smem, stream);
+  return launch_k(k_group_place, grid, kPlaceThreads, smem, stream, true, p);
 }
 
 }  // namespace moe
