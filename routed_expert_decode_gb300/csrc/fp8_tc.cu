@@ -12,12 +12,13 @@
 // packed FMA, and a row's quantisation block after SwiGLU is a maximum over two
 // threads' registers.
 //
-// What bounds it: that epilogue.  Its 32768 FMAs and 128 KB of TMEM reads a block
-// take ~340 clocks of the SM's four schedulers against the MMA's 512, but the chain MMA
-// -> loads -> FMAs -> release -> MMA, with two accumulators to hide it in, comes to ~950.
-// 16384 rows of gate/up (d 6144, f 2048, 16 experts): 430 us, 1.92 PFLOP/s; 4000 x
-// 4096 x 6144 dense: 115 us, 1.75 PFLOP/s.  Without the epilogue the same tiles take 332 and
-// 75 us, of which the second is L2's bandwidth (48 KB a block and SM, 16 TB/s).
+// What bounds it: the chain MMA -> loads -> FMAs -> release -> MMA with two
+// accumulators to hide it in, ~850 clocks a block against the MMA's 512; the
+// epilogue's 32768 FMAs and 128 KB of TMEM reads need ~340 of the SM's schedulers.
+// Latency of single instructions counts in it, so the buffers are addressed as shared
+// memory and the roles branch on a uniform warp number (through generic addresses 430
+// us and 115, on tid / 32 377 and 107).  16384 rows of gate/up (d 6144, f 2048, 16
+// experts): 360 us, 2.29 PFLOP/s; 4000 x 4096 x 6144 dense: 90 us, 2.23 PFLOP/s.
 // Measured and not kept: pairs of CTAs on 256 rows (cta_group::2, which halves an SM's
 // weight bytes: 504 and 122 against 476 and 119 us -- the other CTA's arrivals lengthen
 // the chain); accumulators of one weight block each, four in flight (494 and 131:
@@ -68,8 +69,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
              const int split_below, const bool vec) {
   pdl_trigger();
   extern __shared__ __align__(1024) uint8_t tsm_raw[];
-  uint8_t *tsm = (uint8_t *)(((uintptr_t)tsm_raw + 1023) & ~(uintptr_t)1023);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t *tsm = tsm_raw + ((0u - s32(tsm_raw)) & 1023u);  // stays a shared address
+  const int tid = threadIdx.x, lane = tid & 31;
+  // through a shuffle, so that the roles' branches are known to be uniform
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   uint8_t *ctrl = tsm + n_stages * kStage;
   uint64_t *full = (uint64_t *)ctrl;     // [kMaxStages] operands of a stage landed
   uint64_t *empty = full + kMaxStages;   // [kMaxStages] ... consumed
@@ -129,8 +132,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp < kEpiWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRole));
-    if (warp == 0) {
-      // ============================ weights (and activations in order)
+    if (warp == 0 || (warp == 2 && !gather)) {
+      // ============================ weights (and activations in order), by warp 0;
+      // the scales by warp 2 where it has no activations to copy
+      const bool scales = gather == (warp == 0);
       Ring st;
       uint32_t slot = 0;
       while (!guard.aborted() && walk.take(seg)) {
@@ -152,12 +157,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const uint32_t s = st.i;
           bar_wait(&empty[s], st.phase ^ 1, guard);  // the first use passes
           if (guard.aborted()) break;
+          if (scales) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) cp4(s32(xsc + slot * kM + lane + 32 * i), xs[i] + kb);
-          if (lane < 2) cp4(s32(wsc + 2 * slot + lane), ws + kb);
-          cp_arrive(&full[s]);
-          slot = (slot + 1) % kScaleSlots;
-          if (lane) continue;
+            for (int i = 0; i < 4; ++i) cp4(s32(xsc + slot * kM + lane + 32 * i), xs[i] + kb);
+            if (lane < 2) cp4(s32(wsc + 2 * slot + lane), ws + kb);
+            cp_arrive(&full[s]);
+            slot = (slot + 1) % kScaleSlots;
+          }
+          if (lane || warp) continue;
           uint8_t *buf = tsm + s * kStage, *dst = buf + kABytes;
           bar_expect(&full[s], bytes);
           if (!gather) tma_x(buf, &maps.x, kb * 128, t.row0, &full[s]);
@@ -167,7 +174,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
       // the stages still in use: leave with no copy in flight
-      for (uint32_t i = 0; i < n_stages; ++i, st.next(n_stages))
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      for (uint32_t i = 0; warp == 0 && i < n_stages; ++i, st.next(n_stages))
         if (!bar_wait_for(*abort_flag ? &full[st.i] : &empty[st.i], st.phase ^ 1))
           atomicOr(a.err, kErrTimeout);
     } else if (warp == 1) {
@@ -262,39 +270,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int i = 0; i < 16; ++i)
             acc[16 * c + i] = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), s2, acc[16 * c + i]);
         };
-        // Two loads of 32 columns are in flight at a time (a wait covers all of a
-        // thread's loads), the next pair issued as registers come free -- across
-        // the blocks too, so that a load's latency lies under the FMAs before it.
+        // One load of 32 columns is in flight while the chunk before it is added (a wait
+        // covers all of a thread's loads), across the blocks too.
         float v0[32], v1[32];
         bar_wait(&d_full[dr.i], dr.phase, guard);
         tc_fence_after();
         tc_ld32(col0 + dr.i * 256, v0);
-        tc_ld32(col0 + dr.i * 256 + 32, v1);
         for (int kb = seg.kb0; kb < seg.kb1; ++kb) {
           const uint32_t col = col0 + dr.i * 256;
           const float sx = xsc[slot * kM + m];
           const float s0 = sx * wsc[2 * slot + (SWIGLU ? 0 : half)];
           const float s1 = SWIGLU ? sx * wsc[2 * slot + 1] : s0;
           slot = (slot + 1) % kScaleSlots;
-          const bool more = kb + 1 < seg.kb1;
           tc_wait_ld32(v0);
-          tie32(v1);
+          tc_ld32(col + 32, v1);
           fma32(v0, 0, s0);
+          tc_wait_ld32(v1);
           tc_ld32(col + kCol2, v0);
           fma32(v1, 1, s0);
-          tc_ld32(col + kCol2 + 32, v1);
           tc_wait_ld32(v0);
-          tie32(v1);
+          tc_ld32(col + kCol2 + 32, v1);
+          fma32(v0, 2, s1);
+          tc_wait_ld32(v1);
           release(dr.i);
           dr.next(2);
-          fma32(v0, 2, s1);
-          if (more) {
+          if (kb + 1 < seg.kb1) {
             bar_wait(&d_full[dr.i], dr.phase, guard);
             tc_fence_after();
             tc_ld32(col0 + dr.i * 256, v0);
           }
           fma32(v1, 3, s1);
-          if (more) tc_ld32(col0 + dr.i * 256 + 32, v1);
         }
       }
       // ---- a share of a tile: the last of its workers adds up all shares

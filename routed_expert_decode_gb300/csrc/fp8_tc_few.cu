@@ -72,12 +72,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               const int split_below) {
   pdl_trigger();
   extern __shared__ __align__(1024) uint8_t tsm_raw[];
-  uint8_t *tsm = (uint8_t *)(((uintptr_t)tsm_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t *tsm = tsm_raw + ((0u - s32(tsm_raw)) & 1023u);  // stays a shared address
   static_assert(!SWIGLU || NB == 2, "gate and up");
   constexpr uint32_t kXBytes = MT * 128, kStage = kXBytes + NB * kWBytes;
   constexpr uint32_t kAccs = 256 / MT;        // accumulators in flight
   constexpr int kC = MT / 2;                  // rows of an epilogue warp
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  // through a shuffle, so that the roles' branches are known to be uniform
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   uint8_t *ctrl = tsm + n_stages * kStage;
   uint64_t *full = (uint64_t *)ctrl;    // [kMaxStages] operands of a stage landed
   uint64_t *empty = full + kMaxStages;  // [kMaxStages] ... consumed
