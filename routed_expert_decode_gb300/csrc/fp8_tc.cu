@@ -18,7 +18,7 @@
 // Latency of single instructions counts in it, so the buffers are addressed as shared
 // memory and the roles branch on a uniform warp number (through generic addresses 430
 // us and 115, on tid / 32 377 and 107).  16384 rows of gate/up (d 6144, f 2048, 16
-// experts): 360 us, 2.29 PFLOP/s; 4000 x 4096 x 6144 dense: 90 us, 2.23 PFLOP/s.
+// experts): 355 us, 2.32 PFLOP/s; 4000 x 4096 x 6144 dense: 85 us, 2.37 PFLOP/s.
 // Measured and not kept: pairs of CTAs on 256 rows (cta_group::2, which halves an SM's
 // weight bytes: 504 and 122 against 476 and 119 us -- the other CTA's arrivals lengthen
 // the chain); accumulators of one weight block each, four in flight (494 and 131:
@@ -34,11 +34,12 @@
 // 4..11 epilogue (warp w reads TMEM lanes 32*(w%4).., columns by half).
 //
 // Work goes out over one CTA per SM: whole tiles in rounds, and the tiles of the last,
-// partial round cut along K into equal shares unless nearly every SM would have one
-// (first in every CTA's order; 16384 rows of gate/up: 476 us split, 484 whole).  The
-// shares of a tile meet in the workspace: each CTA writes its fp32 sums, the last one to
-// arrive adds all of them in ascending K, so the result does not depend on the
-// order of arrival.
+// partial round in two shares along K if every share finds a CTA and K is long.  The
+// shares of a tile meet in the workspace: each CTA writes its fp32 sums, the second to
+// arrive adds the other's; a sum of two does not depend on their order.  A meeting takes
+// ~6.5 us, mostly for 128 KB out of an SM and into another.  Columns 4096, K 6144, 16, 160
+// and 512 tiles: 19.9, 42.4 and 85.3 us split, 22.3, 44.5 and 87.0 whole; K 2048, 16
+// tiles: 13.3 split, 10.6 whole; four shares of K 6144: 22.0, 43.5 and 85.6.
 #include <string.h>
 
 #include "fp8_tc_ptx.cuh"
@@ -50,6 +51,7 @@ constexpr int kTcThreads = 12 * 32;
 constexpr uint32_t kTcStages = 4;  // of the operand ring, at most
 constexpr int kEpiWarp0 = 4;
 constexpr int kM = 128;  // rows of a tile
+constexpr int kSplitBlocks = 40;  // blocks of K from which a tile of the last round is split
 // Scales of the blocks of K in flight.  A block's are written when the MMA a ring of
 // stages earlier is done, which was issued when the epilogue had read the block two
 // before that: the slot of the block two further back is free.
@@ -60,13 +62,35 @@ constexpr uint32_t kABytes = kM * 128, kStage = kABytes + 2 * kWBytes;
 // with 56 the activations' row numbers spill (437 against 429 us)
 constexpr int kRegsRole = 72, kRegsEpi = 216;
 
+// A CTA's work: half of a split tile, then whole tiles.
+struct TileWalk {
+  int n_all, kbs, grid, worker, next;
+  bool half;  // half a tile is to come
+  __device__ TileWalk(int n_all_, const Fp8Args &a, int worker_, int grid_)
+      : n_all(n_all_), kbs((int)a.nbk), grid(grid_), worker(worker_) {
+    const int rest = n_all - grid * (int)quotient(n_all, grid, a.workers_inv);
+    const bool split = 2 * rest <= grid && kbs >= kSplitBlocks;
+    half = split && worker < 2 * rest;
+    next = (split ? rest : 0) + worker;
+  }
+  __device__ bool take(Seg &s) {
+    if (!half && next >= n_all) return false;
+    s.tile = half ? worker >> 1 : next;
+    s.kb0 = half && (worker & 1) ? kbs >> 1 : 0;
+    s.kb1 = half && !(worker & 1) ? kbs >> 1 : kbs;
+    if (!half) next += grid;
+    half = false;
+    return true;
+  }
+};
+
 // A row's product over one segment leaves 128 fp32 sums in each of its two epilogue
 // threads: acc[0..31] and acc[32..63] are pairs of columns -- of the gate and the
 // up block (SwiGLU), or of a block's two halves.
 template <bool SWIGLU>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_fp8_tc(const Fp8Args a, const __grid_constant__ Fp8Maps maps, const uint32_t n_stages,
-             const int split_below, const bool vec) {
+             const bool vec) {
   pdl_trigger();
   extern __shared__ __align__(1024) uint8_t tsm_raw[];
   uint8_t *tsm = tsm_raw + ((0u - s32(tsm_raw)) & 1023u);  // stays a shared address
@@ -123,7 +147,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   pdl_wait();
   const RowTiles rt = fp8_row_tiles<kM>(a, tiles_sm);
   const int worker = (int)blockIdx.x;
-  Walk walk(rt.total * (int)a.n_tiles, a, worker, (int)gridDim.x, split_below);
+  TileWalk walk(rt.total * (int)a.n_tiles, a, worker, (int)gridDim.x);
   Seg seg;
   const Guard guard{a.err, abort_flag};
   auto my_tile = [&](int v) { return fp8_tile<kM>(a, rt, v); };
@@ -302,45 +326,38 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           fma32(v1, 3, s1);
         }
       }
-      // ---- a share of a tile: the last of its workers adds up all shares
+      // ---- half a tile: add the other half, or leave the sums to it
       if (seg.kb1 - seg.kb0 < (int)a.nbk) {
         if (quarter * 32 >= t.rows) continue;  // both warps of the pair
-        const int c0 = walk.first_worker(seg.tile);
-        const int n = walk.last_worker(seg.tile) - c0 + 1;
-        // part of worker c: its second slot if it starts the tile, its first otherwise
-        auto part = [&](int c) {
-          return (float4 *)(a.part + (size_t)(2 * c + (c == c0)) * a.part_stride) +
+        auto part = [&](int w) {
+          return (float4 *)(a.part + (size_t)w * a.part_stride) +
                  (size_t)(quarter * 2 + half) * 1024 + lane;
         };
-        float4 *mine = part(worker);
+        float4 *to = part(worker);
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          __stcg(mine + 32 * i,
+          __stcg(to + 32 * i,
                  make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y));
         __threadfence();
         meet();
-        uint32_t *count = a.sync + 4 * seg.tile + quarter;
         if (half == 0 && lane == 0) {
+          uint32_t *count = a.sync + 4 * seg.tile + quarter;
           __threadfence();
-          const bool last = atomicAdd(count, 1u) == (uint32_t)n - 1;
-          if (last) atomicExch(count, 0u);
-          last_part[quarter] = last;
+          const bool second = atomicAdd(count, 1u) == 1u;
+          if (second) atomicExch(count, 0u);
+          last_part[quarter] = second;
         }
         meet();
         if (!last_part[quarter]) continue;
         __threadfence();
+        const float4 *from = part(worker ^ 1);
 #pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
-        for (int p = 0; p < n; ++p) {
-          const float4 *src = part(c0 + p);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float4 v = __ldcg(src + 32 * i);
-            acc[2 * i].x += v.x;
-            acc[2 * i].y += v.y;
-            acc[2 * i + 1].x += v.z;
-            acc[2 * i + 1].y += v.w;
-          }
+        for (int i = 0; i < 32; ++i) {
+          const float4 v = __ldcg(from + 32 * i);
+          acc[2 * i].x += v.x;
+          acc[2 * i].y += v.y;
+          acc[2 * i + 1].x += v.z;
+          acc[2 * i + 1].y += v.w;
         }
       }
       // ---- outputs
@@ -455,8 +472,7 @@ cudaError_t run_tc(Fp8Args &a, cudaStream_t stream) {
   static int set[kMaxDevices];
   const cudaError_t e = allow_smem(kern, smem, set);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, sms, kTcThreads, smem, stream, true, a, maps, (uint32_t)ns, sms * 7 / 8,
-                  vec);
+  return launch_k(kern, sms, kTcThreads, smem, stream, true, a, maps, (uint32_t)ns, vec);
 }
 
 }  // namespace

@@ -14,11 +14,11 @@ size_t fp8_tc_ws(uint32_t rows);
 cudaError_t launch_fp8_tc(Fp8Args &a, bool swiglu, cudaStream_t stream);
 cudaError_t launch_fp8_few(Fp8Args &a, bool swiglu, cudaStream_t stream);
 // The call's rows an expert, on average, choose the kernel and the few-row one's tile.
-// 32 experts, 4096 x 2048 (us; tiles of up to 32 and 64 rows of the few-row kernel, the
-// many-row kernel):
-//   rows         16            32            48            64            96
-//   gate/up   90  94 100    88 100 104   100 103 106   120 116 109   163 145 116
-//   down      48  48  61    59  51  63    80  52  64    96  59  67   134  71  72
+// 32 experts, 4096 x 2048 (us; the few-row kernel's tiles of up to 32 rows, for the down
+// product also of up to 64, and the many-row kernel):
+//   rows       16        32        48        64        96       128
+//   gate/up  87  92    87  95    94  97   107  99   140 105   182 130
+//   down    47 47 53  48 49 55  59 50 56  71 54 59  99 61 65  126 76 66
 constexpr uint64_t kFp8FewSwiglu = 48;  // tiles of 32 rows up to here
 constexpr uint64_t kFp8FewProduct32 = 24, kFp8FewProduct64 = 96;
 

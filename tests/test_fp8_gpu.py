@@ -377,6 +377,20 @@ def test_swiglu(fp8, T, E, k, K, N, empty):
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
 
 
+# tiles of 128 rows whose last round is shared along K by pairs of CTAs: K of 40 blocks and
+# more, from the last block short to a few tiles more than the 152 of a whole round
+@pytest.mark.parametrize("T,E,k,K,N,empty", [
+    (300, 1, 1, 5120, 256, ()),
+    (130, 1, 1, 5136, 330, ()),
+    (310, 3, 2, 5232, 130, ()),
+    (2500, 1, 1, 5136, 2048, ()),
+])
+def test_product_and_swiglu_in_halves_of_a_tile(fp8, T, E, k, K, N, empty):
+    test_product(fp8, "bf16", T, E, k, K, N, empty)
+    if N < 2048:
+        test_swiglu(fp8, T, E, k, K, N, empty)
+
+
 def test_product_planes_off_their_alignment(fp8):
     """Code planes that start off a 16-byte boundary give the aligned planes' values."""
     rng = np.random.default_rng(2)
