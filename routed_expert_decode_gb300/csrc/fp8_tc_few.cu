@@ -450,12 +450,13 @@ cudaError_t run_few(Fp8Args &a, cudaStream_t stream) {
   static int set[kMaxDevices];
   const cudaError_t e = allow_smem(kern, smem, set);
   if (e != cudaSuccess) return e;
-  // Tiles are split along K only when they leave three SMs of four idle: 64 SMs
-  // already draw 5.4 TB/s, and under a saturated HBM each of the split's round trips
-  // (shares out, count, shares in) takes ~3 us.  16 tiles of 48 blocks: 10.5 us split,
-  // 22.4 whole; 64 tiles: 25.7 split, 23.6 whole.
+  // Tiles are split along K when they leave three SMs of four idle and K has 16 blocks:
+  // 64 SMs already draw 5.4 TB/s, and under a saturated HBM each of the split's round
+  // trips (shares out, count, shares in) takes ~3 us.  Tiles of 128 columns, split and
+  // whole: K 6144, 4 tiles 7.4 and 13.5 us, 32 tiles 10.6 and 13.8, 64 tiles 16.9 and 14.7;
+  // K 2048, 4 tiles 5.9 and 6.3; K 1024, 4 tiles 5.6 and 4.8.
   return launch_k(kern, sms, kFewThreads, smem, stream, true, a, maps, (uint32_t)ns,
-                  sms / 4);
+                  a.nbk >= 16 ? sms / 4 : 0);
 }
 
 }  // namespace
@@ -464,11 +465,11 @@ cudaError_t launch_fp8_few(Fp8Args &a, bool swiglu, cudaStream_t stream) {
   const uint64_t R = a.R, E = a.E;
   if (swiglu) return run_few<true, 32, 2>(a, stream);
   if (R > kFp8FewProduct32 * E) return run_few<false, 64, 2>(a, stream);
-  // At most this many pairs of weight blocks have rows.  Few rounds of tiles go out
-  // more evenly one block a tile (one token's down projection, 192 pairs: 22.0
-  // against 23.1 us); with many rounds a pair shares a tile's fixed work.
+  // At most this many pairs of weight blocks have rows.  Where every block finds an SM,
+  // one a tile draws from more of them (K 2048, 48 pairs: 7.2 against 8.0 us); beyond, a
+  // pair shares a tile's fixed work (96 pairs: 13.6 against 11.9 us).
   const uint64_t pairs = (R < E ? R : E) * ((a.nbn + 1) / 2);
-  return pairs <= 4 * (uint64_t)fp8_ctas() ? run_few<false, 32, 1>(a, stream)
+  return 2 * pairs <= (uint64_t)fp8_ctas() ? run_few<false, 32, 1>(a, stream)
                                            : run_few<false, 32, 2>(a, stream);
 }
 
