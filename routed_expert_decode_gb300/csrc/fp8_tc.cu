@@ -1,5 +1,5 @@
 // fp8_tc.cu -- routed and dense products over block-scaled e4m3 operands on the
-// 5th-generation tensor cores, for experts with many rows: bound by arithmetic.
+// 5th-generation tensor cores, for experts with many rows: bound by L2 and arithmetic.
 //
 // A tile is 128 activation rows of one expert by two blocks of 128 weight rows (256
 // columns of the product, or the gate and up rows of one block of 128 features).
@@ -12,13 +12,14 @@
 // packed FMA, and a row's quantisation block after SwiGLU is a maximum over two
 // threads' registers.
 //
-// What bounds it: the chain MMA -> loads -> FMAs -> release -> MMA with two
-// accumulators to hide it in, ~850 clocks a block against the MMA's 512; the
-// epilogue's 32768 FMAs and 128 KB of TMEM reads need ~340 of the SM's schedulers.
-// Latency of single instructions counts in it, so the buffers are addressed as shared
-// memory and the roles branch on a uniform warp number (through generic addresses 430
-// us and 115, on tid / 32 377 and 107).  16384 rows of gate/up (d 6144, f 2048, 16
-// experts): 355 us, 2.32 PFLOP/s; 4000 x 4096 x 6144 dense: 85 us, 2.37 PFLOP/s.
+// What bounds it: the operands' way into the SM.  16384 rows of gate/up (d 6144, f 2048,
+// 16 experts) take 339 us, 2.43 PFLOP/s, and 310 with an epilogue that only releases the
+// accumulators; 4000 x 4096 x 6144 dense 81 us, 2.48 PFLOP/s, and 77.  48 KB a block in
+// ~900 clocks is 52 of the 64 bytes a clock that L2 gives an SM.  (Under a steady stream
+// of calls the card's power cap adds 5-10 %.)  The chain MMA -> loads -> FMAs -> release ->
+// MMA with two accumulators to hide it in comes next, so the latency of single
+// instructions counts: the buffers are addressed as shared memory and the roles branch on
+// a uniform warp number (through generic addresses 430 us and 115, on tid / 32 377 and 107).
 // Measured and not kept: pairs of CTAs on 256 rows (cta_group::2, which halves an SM's
 // weight bytes: 504 and 122 against 476 and 119 us -- the other CTA's arrivals lengthen
 // the chain); accumulators of one weight block each, four in flight (494 and 131:
@@ -46,6 +47,13 @@
 
 namespace moe {
 namespace {
+
+// a product that stays where it is written: after the loads of its factors have had time
+__device__ __forceinline__ float mul_here(float a, float b) {
+  float r;
+  asm volatile("mul.rn.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 constexpr int kTcThreads = 12 * 32;
 constexpr uint32_t kTcStages = 4;  // of the operand ring, at most
@@ -288,42 +296,52 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         slot = (slot + seg.kb1 - seg.kb0) % kScaleSlots;
       } else {
-        auto fma32 = [&](const float (&v)[32], int c, float s) {
+        // columns 32c + 2 [i0, i1) of this warp's, scaled, to the sums
+        auto fma = [&](const float (&v)[32], int c, int i0, int i1, float s) {
           const float2 s2 = make_float2(s, s);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
+          for (int i = i0; i < i1; ++i)
             acc[16 * c + i] = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), s2, acc[16 * c + i]);
         };
         // One load of 32 columns is in flight while the chunk before it is added (a wait
-        // covers all of a thread's loads), across the blocks too.
-        float v0[32], v1[32];
+        // covers all of a thread's loads), across the blocks too.  The next block's
+        // barrier is looked at, and its scales loaded, under the last chunk's FMAs
+        // (gate/up 357 -> 347 us; a look that may suspend the warp: 370).
+        float v0[32], v1[32], sx, w0, w1 = 0.0f;
+        auto scales = [&]() {
+          sx = xsc[slot * kM + m];
+          w0 = wsc[2 * slot + (SWIGLU ? 0 : half)];
+          if (SWIGLU) w1 = wsc[2 * slot + 1];
+          slot = (slot + 1) % kScaleSlots;
+        };
         bar_wait(&d_full[dr.i], dr.phase, guard);
         tc_fence_after();
         tc_ld32(col0 + dr.i * 256, v0);
+        scales();
         for (int kb = seg.kb0; kb < seg.kb1; ++kb) {
           const uint32_t col = col0 + dr.i * 256;
-          const float sx = xsc[slot * kM + m];
-          const float s0 = sx * wsc[2 * slot + (SWIGLU ? 0 : half)];
-          const float s1 = SWIGLU ? sx * wsc[2 * slot + 1] : s0;
-          slot = (slot + 1) % kScaleSlots;
+          const float s0 = mul_here(sx, w0), s1 = SWIGLU ? mul_here(sx, w1) : s0;
           tc_wait_ld32(v0);
           tc_ld32(col + 32, v1);
-          fma32(v0, 0, s0);
+          fma(v0, 0, 0, 16, s0);
           tc_wait_ld32(v1);
           tc_ld32(col + kCol2, v0);
-          fma32(v1, 1, s0);
+          fma(v1, 1, 0, 16, s0);
           tc_wait_ld32(v0);
           tc_ld32(col + kCol2 + 32, v1);
-          fma32(v0, 2, s1);
+          fma(v0, 2, 0, 16, s1);
           tc_wait_ld32(v1);
           release(dr.i);
           dr.next(2);
+          const bool ready = bar_test(&d_full[dr.i], dr.phase);
+          fma(v1, 3, 0, 8, s1);
           if (kb + 1 < seg.kb1) {
-            bar_wait(&d_full[dr.i], dr.phase, guard);
+            if (!ready) bar_wait(&d_full[dr.i], dr.phase, guard);
             tc_fence_after();
             tc_ld32(col0 + dr.i * 256, v0);
+            scales();
           }
-          fma32(v1, 3, s1);
+          fma(v1, 3, 8, 16, s1);
         }
       }
       // ---- half a tile: add the other half, or leave the sums to it
@@ -363,35 +381,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // ---- outputs
       const int r = t.row0 + m;
       if (!SWIGLU) {
-        if (!live) continue;
+        if (!warp_live) continue;
         const uint32_t n0 = (uint32_t)(t.nt * 2 + half) * 128;
+        // Chunks of 32 bytes of a row.  Two lanes exchange one of each two of theirs, so
+        // that a store covers 64 bytes of 16 rows and not 32 of 32 (4000 x 4096 dense: 84.4
+        // -> 82.3 us; four lanes and 128 bytes: the same).
+        auto store = [&](auto *out, auto pack) {
+          constexpr int kC = 32 / sizeof(*out);  // columns of a chunk
+          const int odd = lane & 1, pm = m - odd;
+#pragma unroll
+          for (int i = 0; i < 128 / kC; i += 2) {
+            uint32_t w[2][8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) w[h][j] = pack((i + h) * 8 + j);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[0][j] : w[1][j], 1);
+              w[0][j] = odd ? got : w[0][j];
+              w[1][j] = odd ? w[1][j] : got;
+            }
+            const uint32_t n = n0 + kC * (i + odd);
+            auto *dst = out + (size_t)(t.row0 + pm) * a.ld + n;
+            if (n < a.N && pm < t.rows) st_global32(dst, w[0]);
+            if (n < a.N && pm + 1 < t.rows) st_global32(dst + a.ld, w[1]);
+          }
+        };
         if (vec && a.odt == MOE_DT_F32) {
-          float *dst = (float *)a.out + (size_t)r * a.ld + n0;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (n0 + 8 * i < a.N) {
-              uint32_t w[8];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                w[2 * j] = __float_as_uint(acc[4 * i + j].x);
-                w[2 * j + 1] = __float_as_uint(acc[4 * i + j].y);
-              }
-              st_global32(dst + 8 * i, w);
-            }
+          store((float *)a.out,
+                [&](int i) { return __float_as_uint(i & 1 ? acc[i / 2].y : acc[i / 2].x); });
+        } else if (vec && a.odt == MOE_DT_BF16) {
+          store((uint16_t *)a.out, [&](int i) { return pack2<MOE_DT_BF16>(acc[i].x, acc[i].y); });
         } else if (vec) {
-          uint16_t *dst = (uint16_t *)a.out + (size_t)r * a.ld + n0;
-          const bool bf = a.odt == MOE_DT_BF16;
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (n0 + 16 * i < a.N) {
-              uint32_t w[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                w[j] = bf ? pack2<MOE_DT_BF16>(acc[8 * i + j].x, acc[8 * i + j].y)
-                          : pack2<MOE_DT_F16>(acc[8 * i + j].x, acc[8 * i + j].y);
-              st_global32(dst + 16 * i, w);
-            }
-        } else {
+          store((uint16_t *)a.out, [&](int i) { return pack2<MOE_DT_F16>(acc[i].x, acc[i].y); });
+        } else if (live) {
 #pragma unroll
           for (int i = 0; i < 64; ++i) {
             if (n0 + 2 * i < a.N) fp8_store(a, r, n0 + 2 * i, acc[i].x);

@@ -40,6 +40,17 @@ __device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
       : "memory");
   return done != 0;
 }
+// the same without suspending the thread
+__device__ __forceinline__ bool bar_test(uint64_t *b, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(s32(b)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 // What a wait that runs out does: it flags the call and sets the CTA's abort flag,
 // after which every wait returns at once.  The work goes on to the end of the
 // segment on whatever the buffers hold, so that a warp's lanes never part in front
