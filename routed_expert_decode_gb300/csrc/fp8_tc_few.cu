@@ -21,8 +21,9 @@
 // a warp maximum, and one word a quarter and row in shared memory.
 //
 // Warps: 0 weights (and rows in order) by TMA, 1 TMEM owner and MMA issuer, 2 routed
-// rows by cp.async through perm, 3 the rows' scales, 4..11 epilogue.  The work is
-// split as in fp8_tc.cu.
+// rows by cp.async through perm, 3 the rows' scales, 4..11 epilogue.  The work
+// goes out over one CTA per SM as Walk says; the shares of a split tile meet in the
+// workspace, where the last to arrive adds all of them in ascending K.
 #include <string.h>
 
 #include "fp8_tc_ptx.cuh"

@@ -1,5 +1,5 @@
-// fp8_tc_ptx.cuh -- what the two tensor-core product kernels share: PTX helpers, the
-// work split, the tensor maps.
+// fp8_tc_ptx.cuh -- what the two tensor-core product kernels share: PTX helpers, a
+// segment of work (and the few-row kernel's split), the tensor maps.
 #pragma once
 
 #include <cuda.h>
@@ -203,12 +203,12 @@ struct Ring {
 };
 
 // ---------------------------------------------------------------- work split
-// A worker (a CTA, or a pair) has in order: its share [pos, end) of the split
-// tiles' K blocks, then whole tiles split, split + G, ...  Every role walks the
-// same list.
+// K blocks kb0 .. kb1 - 1 of a tile
 struct Seg {
   int tile, kb0, kb1;
 };
+// A CTA has in order: its share [pos, end) of the split tiles' K blocks, then whole
+// tiles split, split + G, ...  Every role walks the same list.
 struct Walk {
   int n_all, share, kbs, grid;  // tiles, K blocks per worker of the split tiles, per tile
   int pos, end, next;

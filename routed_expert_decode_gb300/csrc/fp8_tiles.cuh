@@ -23,7 +23,7 @@ struct Fp8Args {
   float *hs;
   int odt;
   uint32_t n_tiles, n_tiles_inv;  // column tiles of an expert, floor((2^32 - 1) / that)
-  uint32_t workers_inv;           // the same of the CTAs (pairs) that share the tiles
+  uint32_t workers_inv;           // the same of the CTAs that share the tiles
   uint32_t *err, *sync;
   float *part;         // partial sums of split tiles
   size_t part_stride;  // floats per part
