@@ -38,7 +38,7 @@
 namespace moe {
 namespace {
 
-constexpr int kGrWarps = 8;  // tokens of a selecting CTA
+constexpr int kGrWarps = 4;  // tokens of a selecting CTA (64 tokens: 7.4 us, 7.6 with 8)
 // A call of one or two tokens runs on k_group_few (256 experts: 5.1 and 5.8 us; 7.7
 // with four tokens, 7.0 on the two kernels).
 constexpr uint32_t kGrFewTokens = 2;

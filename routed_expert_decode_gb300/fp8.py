@@ -93,12 +93,13 @@ def _stream(stream, t: torch.Tensor):
     return _raw_stream(t.get_device()) if stream is None else moe._stream(stream)
 
 
-def _rows2d(t: torch.Tensor, name: str):
-    """(pointer, dtype code, row stride) of a 2-d CUDA tensor with consecutive columns."""
+def _rows2d(t: torch.Tensor, cols: int, name: str):
+    """(pointer, dtype code, row stride) of a 2-d CUDA tensor with consecutive columns, which
+    number ``cols``."""
     dt = DTYPES.get(t.dtype)
     ld, step = t.stride()
-    if dt is None or step != 1 or ld < t.shape[1] or not t.is_cuda:
-        rows, cols = t.shape
+    if dt is None or step != 1 or ld < cols or not t.is_cuda:
+        rows = t.shape[0]
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
         if dt is None:
@@ -123,12 +124,13 @@ def _plane(t: torch.Tensor, dtypes, shape, name: str) -> int:
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
-_U8 = (torch.uint8,)
 
 
 def _ws(ws: torch.Tensor):
-    n = ws.numel()
-    return _plane(ws, _U8, (n,), "ws"), n
+    if ws.dtype is torch.uint8 and ws.is_contiguous() and ws.is_cuda:
+        return ws.data_ptr(), ws.numel()
+    raise ValueError(f"ws must be a contiguous CUDA tensor of torch.uint8, got {ws.dtype} on "
+                     f"{ws.device}")
 
 
 # ------------------------------------------------------------------ router
@@ -151,7 +153,7 @@ def group_route(router: MoeRouter, logits, bias: Optional[torch.Tensor], idx, w,
     k = router.top_k
     if E != router.n_expert:
         raise ValueError(f"logits must have {router.n_expert} columns, got {E}")
-    lp, dt, ld = _rows2d(logits, "logits")
+    lp, dt, ld = _rows2d(logits, E, "logits")
     wsp, wsn = _ws(ws)
     st = (_lib or lib()).moe_group_route(
         ctypes.byref(router), lp, dt, ld,
@@ -168,7 +170,7 @@ def quantize(x, q, scale, stream=None) -> None:
     """moe_fp8_quantize: rows of ``x`` [T, d] to e4m3 codes ``q`` [T, d] and fp32
     scales ``scale`` [T, ceil(d / 128)]."""
     T, d = x.shape
-    xp, dt, ld = _rows2d(x, "x")
+    xp, dt, ld = _rows2d(x, d, "x")
     st = (_lib or lib()).moe_fp8_quantize(xp, dt, ld, T, d, _plane(q, _CODES, (T, d), "q"),
                                 _plane(scale, _F32, (T, blocks(d)), "scale"),
                                 _stream(stream, x))
@@ -212,7 +214,7 @@ def product(w: Mat, xq, xs, out, ws, off=None, perm=None, top_k: int = 1, stream
     R, N = out.shape
     if N != w.N:
         raise ValueError(f"out must have {w.N} columns, got {N}")
-    op, dt, ld = _rows2d(out, "out")
+    op, dt, ld = _rows2d(out, N, "out")
     x = _activation(w, xq, xs, R, off, perm, top_k)
     wsp, wsn = _ws(ws)
     st = (_lib or lib()).moe_fp8_product(w.ref, w.E, N, w.K, ctypes.byref(x), op, dt, ld, wsp, wsn,
@@ -243,14 +245,15 @@ def combine(o, w, pos, y, shared=None, stream=None) -> None:
     """moe_fp8_combine: ``y`` [T, d] = ``shared`` [T, d] + sum over slots j of
     ``w`` [T, k] * ``o`` [R, d] at row ``pos`` [T, k]."""
     T, d = y.shape
-    R, k = o.shape[0], pos.shape[1]
-    if o.shape[1] != d or (shared is not None and shared.shape != (T, d)):
+    R, do = o.shape
+    k = pos.shape[1]
+    if do != d or (shared is not None and shared.shape != (T, d)):
         raise ValueError(f"o and shared must have {d} columns, shared {T} rows")
-    op, dt, ldo = _rows2d(o, "o")
-    yp, ydt, ldy = _rows2d(y, "y")
+    op, dt, ldo = _rows2d(o, d, "o")
+    yp, ydt, ldy = _rows2d(y, d, "y")
     sp, lds = None, 0
     if shared is not None:
-        sp, sdt, lds = _rows2d(shared, "shared")
+        sp, sdt, lds = _rows2d(shared, d, "shared")
         if sdt != dt:
             raise ValueError("shared must have o's type")
     st = (_lib or lib()).moe_fp8_combine(op, dt, ldo, R, _plane(w, _F32, (T, k), "w"),
