@@ -130,10 +130,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int i = 0; i < kMaxStages; ++i) {
       // the TMA producer, its warp's scales, and warps 2 and 3
       bar_init(&full[i], 1 + 32 + (gather ? 64 : 0));
-      bar_init(&empty[i], 1);
+      bar_init(&empty[i], 2);  // the MMAs' reads, and the MMA warp
     }
     for (int i = 0; i < 2; ++i) {
-      bar_init(&d_full[i], 1);
+      bar_init(&d_full[i], 2);  // the MMAs' results, and the MMA warp
       bar_init(&d_empty[i], 8);
     }
     for (int i = 0; i < 4; ++i) bar_init(&pair[i], 2);
@@ -225,6 +225,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc_mma_block(tmem + acc.i * 256, sw128_desc(buf), sw128_desc(buf + kABytes), idesc);
           tc_commit(&empty[st.i]);
           tc_commit(&d_full[acc.i]);
+          // The scales' way through shared memory: their copies (full, waited for
+          // above) come before the epilogue's loads of them, and its loads of two
+          // blocks ago (d_empty, likewise) before the copies into their slots.
+          bar_arrive_elect(&empty[st.i]);
+          bar_arrive_elect(&d_full[acc.i]);
         }
       }
       if (guard.aborted()) {  // else the epilogue has waited for every MMA

@@ -26,6 +26,15 @@ __device__ __forceinline__ void bar_init(uint64_t *b, uint32_t n) {
 __device__ __forceinline__ void bar_arrive(uint64_t *b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(s32(b)) : "memory");
 }
+// the same by one lane of a converged warp, without a branch.  What each lane has
+// waited for happens before what the barrier's waiters do next: a tcgen05.commit's
+// arrival, which an asynchronous operation makes, does not carry that on.
+__device__ __forceinline__ void bar_arrive_elect(uint64_t *b) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(s32(b))
+      : "memory");
+}
 __device__ __forceinline__ void bar_expect(uint64_t *b, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(s32(b)), "r"(bytes)
                : "memory");
