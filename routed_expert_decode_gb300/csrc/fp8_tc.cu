@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (gather) fence_async();
           bar_wait(&d_empty[acc.i], acc.phase ^ 1, guard);
           tc_fence_after();
+          __syncwarp();
           tc_mma_block(tmem + acc.i * 256, sw128_desc(buf), sw128_desc(buf + kABytes), idesc);
           tc_commit(&empty[st.i]);
           tc_commit(&d_full[acc.i]);
@@ -321,6 +322,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         };
         bar_wait(&d_full[dr.i], dr.phase, guard);
         tc_fence_after();
+        __syncwarp();  // each lane waits for itself, the load takes the whole warp
         tc_ld32(col0 + dr.i * 256, v0);
         scales();
         for (int kb = seg.kb0; kb < seg.kb1; ++kb) {
@@ -343,6 +345,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (kb + 1 < seg.kb1) {
             if (!ready) bar_wait(&d_full[dr.i], dr.phase, guard);
             tc_fence_after();
+            __syncwarp();
             tc_ld32(col0 + dr.i * 256, v0);
             scales();
           }

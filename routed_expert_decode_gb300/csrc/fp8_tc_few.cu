@@ -282,6 +282,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           sa = wa[kn];  // on the way while this block is added
           bar_wait(&d_full[dr.i], dr.phase, guard);
           tc_fence_after();
+          __syncwarp();  // each lane waits for itself, the loads take the whole warp
           if (NB == 2) sb = wb[kn];
           Cols<NC> v[NB];
           const uint32_t base = tmem + col0 + dr.i * NB * MT;
