@@ -289,7 +289,7 @@ class Layer:
     ``gate``, ``up`` [E, f, d] and ``down`` [E, d, f] are ``Mat``; ``shared`` is a
     triple of one-expert ``Mat`` or None.  Buffers and the workspace are kept per number
     of tokens and type, as ``moe.Layer`` keeps its own; calls that overlap need layers
-    (or streams' orders) of their own.
+    (or streams' orders) of their own.  What a call makes, it makes on its stream.
     """
 
     def __init__(self, router: MoeRouter, gate: Mat, up: Mat, down: Mat, shared=None):
@@ -306,9 +306,12 @@ class Layer:
         self.router, self.gate, self.up, self.down, self.shared = router, gate, up, down, shared
         self.E, self.f, self.d = gate.E, gate.N, gate.K
         self._buffers = {}
+        self._used_on = {}  # handles of the streams that may use each set
 
     def buffers(self, T: int, dtype: torch.dtype) -> dict:
+        """The buffers of calls of T tokens of a type, made on the current stream if new."""
         key = (T, dtype)
+        here = _raw_stream(self.gate.q.get_device())
         if key not in self._buffers:
             E, k, d, f, R = self.E, self.router.top_k, self.d, self.f, T * self.router.top_k
 
@@ -328,28 +331,41 @@ class Layer:
             n = max(group_route_workspace_size(self.router, T), workspace_size(max(R, T)))
             b["ws"] = torch.zeros(n, dtype=torch.uint8, device=self.gate.q.device)
             self._buffers[key] = b
+            self._used_on[key] = {here}
+        elif here not in self._used_on[key]:
+            moe._used_here(self._used_on[key],
+                           [t for t in self._buffers[key].values() if t is not None],
+                           self.gate.q.device)
         return self._buffers[key]
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor,
                 bias: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
                 stream=None) -> LayerOutput:
-        """y [T, d] of x [T, d] and its router logits [T, E]; y has x's type unless given."""
+        """y [T, d] of x [T, d] and its router logits [T, E]; y has x's type unless given.  With a
+        ``stream`` the whole call runs there, and what it makes belongs to it."""
+        if stream is not None:
+            caller = torch.cuda.current_stream(self.gate.q.device)
+            with moe._on_stream(stream, self.gate.q.device):
+                out = self.forward(x, logits, bias, y)
+            if y is None:  # of the stream's memory, and the caller's to read
+                out.y.record_stream(caller)
+            self.buffers(x.shape[0], x.dtype)
+            return out
         T = x.shape[0]
         k = self.router.top_k
         b = self.buffers(T, x.dtype)
         if y is None:
             y = torch.empty((T, self.d), dtype=x.dtype, device=x.device)
         ws = b["ws"]
-        group_route(self.router, logits, bias, b["idx"], b["w"], b["off"], b["perm"], b["pos"], ws,
-                    stream)
-        quantize(x, b["xq"], b["xs"], stream)
+        group_route(self.router, logits, bias, b["idx"], b["w"], b["off"], b["perm"], b["pos"], ws)
+        quantize(x, b["xq"], b["xs"])
         swiglu(self.gate, self.up, b["xq"], b["xs"], b["hq"], b["hs"], ws, off=b["off"],
-               perm=b["perm"], top_k=k, stream=stream)
-        product(self.down, b["hq"], b["hs"], b["o"], ws, off=b["off"], stream=stream)
+               perm=b["perm"], top_k=k)
+        product(self.down, b["hq"], b["hs"], b["o"], ws, off=b["off"])
         if self.shared is not None:
             sg, su, sd = self.shared
-            swiglu(sg, su, b["xq"], b["xs"], b["shq"], b["shs"], ws, stream=stream)
-            product(sd, b["shq"], b["shs"], b["shared"], ws, stream=stream)
-        combine(b["o"], b["w"], b["pos"], y, shared=b["shared"], stream=stream)
+            swiglu(sg, su, b["xq"], b["xs"], b["shq"], b["shs"], ws)
+            product(sd, b["shq"], b["shs"], b["shared"], ws)
+        combine(b["o"], b["w"], b["pos"], y, shared=b["shared"])
         return LayerOutput(y=y, **{n: b[n] for n in ("idx", "w", "off", "perm", "pos", "xq", "xs",
                                                      "hq", "hs", "o", "shared")})

@@ -183,6 +183,26 @@ def _stream(stream) -> Optional[int]:
     return int(stream)
 
 
+def _on_stream(stream, device):
+    """Context in which ``stream`` (a torch.cuda.Stream or a raw handle) is torch's current one,
+    so that memory made inside belongs to it and is filled in its order."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        stream = (torch.cuda.ExternalStream(handle, device=device) if handle
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
+def _used_here(used_on: set, tensors, device) -> None:
+    """The current stream uses these tensors: memory belongs to the stream it was made on, and
+    has to outlast the work of every other.  ``used_on``: handles of the streams known so far."""
+    stream = torch.cuda.current_stream(device)
+    if stream.cuda_stream not in used_on:
+        used_on.add(stream.cuda_stream)
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def _dev_ptr(t: Optional[torch.Tensor], dtype=None, name="tensor"):
     if t is None:
         return None

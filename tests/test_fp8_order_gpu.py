@@ -42,3 +42,85 @@ def test_scales_meet_their_block(fp8, T, N, gathered):  # noqa: F811
         want = np.repeat(a[xrow] @ b.T, 128, 1)[:, :N]
         assert np.array_equal(out.double().cpu().numpy(), want)
     assert fp8.check_device_error(ws) == 0
+
+
+# ---------------------------------------------------------------- the layer on a stream
+def make_layer(fp8, seed=0, E=8, k=2, d=2048, f=256, **kw):  # noqa: F811
+    """A layer whose products of few rows are shared along K (16 blocks, few tiles)."""
+    from test_fp8_gpu import make_mat
+
+    rng = np.random.default_rng(seed)
+    mats = [make_mat(fp8, rng, E, f, d)[2], make_mat(fp8, rng, E, f, d)[2],
+            make_mat(fp8, rng, E, d, f)[2]]
+    sh = tuple(make_mat(fp8, rng, 1, n, m)[2] for n, m in ((f, d), (f, d), (d, f)))
+    return fp8.Layer(fp8.make_router(E, k, 4, 2, s=2.5), *mats, shared=sh, **kw)
+
+
+def layer_inputs(T, d=2048, E=8, seed=1):
+    rng = np.random.default_rng(seed + T)
+    return (dev(2 * rng.standard_normal((T, d)).astype(np.float32)).bfloat16(),
+            dev(rng.standard_normal((T, E)).astype(np.float32)),
+            dev((0.1 * rng.standard_normal(E)).astype(np.float32)))
+
+
+SLEEP = 1 << 29  # clocks, about a quarter of a second
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("T", [1, 40])
+def test_layer_first_call_on_a_side_stream(fp8, monkeypatch, T, raw):  # noqa: F811
+    """A first call on a stream makes and clears its buffers there, whatever the current
+    stream still has to do and whatever the memory held."""
+    args = layer_inputs(T)
+    want = make_layer(fp8).forward(*args).y.cpu()
+    layer, side = make_layer(fp8), torch.cuda.Stream()
+    zeros, made_on = torch.zeros, []
+    monkeypatch.setattr(torch, "zeros", lambda *a, **kw: (
+        made_on.append(torch.cuda.current_stream().cuda_stream), zeros(*a, **kw))[1])
+    with torch.cuda.stream(side):  # what the stream's memory holds
+        torch.full((fp8.workspace_size(4 * T) + (1 << 20),), 0x55, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(SLEEP)
+    out = layer.forward(*args, stream=side.cuda_stream if raw else side)
+    side.synchronize()
+    assert not torch.cuda.current_stream().query()  # it is still busy
+    assert made_on and set(made_on) == {side.cuda_stream}
+    with torch.cuda.stream(side):
+        assert torch.equal(out.y.cpu(), want)
+        assert fp8.check_device_error(layer.buffers(T, args[0].dtype)["ws"]) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(layer.forward(*args).y.cpu(), want)  # and on the current stream after it
+
+
+def test_layer_output_outlasts_its_stream(fp8):  # noqa: F811
+    """A y that is dropped while its stream still has to write it is not handed out again."""
+    layer, side, args = make_layer(fp8), torch.cuda.Stream(), layer_inputs(40)
+    layer.forward(*args)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(SLEEP)
+    out = layer.forward(*args, stream=side)
+    at = out.y.data_ptr()
+    del out
+    other = [torch.zeros((40, 2048), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    assert not side.query()
+    assert at not in [t.data_ptr() for t in other]
+    torch.cuda.synchronize()
+    assert not any(t.any() for t in other)
+
+
+def test_layer_buffers_outlast_every_stream_that_used_them(fp8):  # noqa: F811
+    """Buffers of a dropped layer wait for the other streams that its calls ran on."""
+    layer, side, args = make_layer(fp8), torch.cuda.Stream(), layer_inputs(300)
+    layer.forward(*args)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(SLEEP)
+    layer.forward(*args, stream=side)
+    b = layer.buffers(300, torch.bfloat16)
+    shape, at = b["o"].shape, b["o"].data_ptr()
+    del layer, b
+    other = [torch.empty(shape, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    assert not side.query()
+    assert at not in [t.data_ptr() for t in other]
+    torch.cuda.synchronize()
