@@ -524,6 +524,7 @@ class Layer:
             setattr(self.weights, n, MoeMat(_dev_ptr(q, None, n + "_q"),
                                            _dev_ptr(sc, torch.float16, n + "_s")))
         self._ws = {}
+        self._used_on = {}  # handles of the streams that may use each workspace
 
     @classmethod
     def from_host(cls, spec, experts: dict, shared: Optional[dict], device):
@@ -549,10 +550,14 @@ class Layer:
                          self.routed_fmt, self.s, flags, self.score)
 
     def workspace(self, T: int, flags=0) -> torch.Tensor:
+        """The workspace of calls of T tokens, made on the current stream if new."""
         key = (T, flags & FLAG_DEBUG_TAPS)
         if key not in self._ws:
             n = workspace_size(self.desc(flags), T)
             self._ws[key] = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.device)
+            self._used_on[key] = {torch.cuda.current_stream(self.device).cuda_stream}
+        else:
+            _used_here(self._used_on[key], (self._ws[key],), self.device)
         return self._ws[key]
 
     def views(self, ws: torch.Tensor, T: int, flags=0) -> dict:
@@ -586,12 +591,17 @@ class Layer:
     def forward(self, x: torch.Tensor, logits: torch.Tensor, bias: torch.Tensor,
                 taps: bool = False, flags: int = 0, y: Optional[torch.Tensor] = None,
                 stream=None) -> LayerOutput:
+        """The layer of x and its router logits.  With a ``stream`` the whole call runs there, and
+        what it makes belongs to it."""
+        if stream is not None:
+            return self._forward_on(stream, x.shape[0], y, flags | (FLAG_DEBUG_TAPS if taps else 0),
+                                    lambda: self.forward(x, logits, bias, taps, flags, y))
         flags = flags | (FLAG_DEBUG_TAPS if taps else 0)
         T = x.shape[0]
         ws = self.workspace(T, flags)
         if y is None:
             y = torch.empty((T, self.d), dtype=torch.float32, device=self.device)
-        layer(self.desc(flags), self.weights, x, logits, bias, y, ws, stream)
+        layer(self.desc(flags), self.weights, x, logits, bias, y, ws)
         v = self.views(ws, T, flags)
         return LayerOutput(y=y, **v)
 
@@ -599,12 +609,25 @@ class Layer:
                        logits: torch.Tensor, taps: bool = False, flags: int = 0,
                        y: Optional[torch.Tensor] = None, stream=None) -> LayerOutput:
         """moe_layer_from_x: the router logits of x (written to ``logits``
-        [T][E]) and the layer on them, in one call."""
+        [T][E]) and the layer on them, in one call; ``stream`` as in ``forward``."""
+        if stream is not None:
+            return self._forward_on(
+                stream, x.shape[0], y, flags | (FLAG_DEBUG_TAPS if taps else 0),
+                lambda: self.forward_from_x(x, w_router, bias, logits, taps, flags, y))
         flags = flags | (FLAG_DEBUG_TAPS if taps else 0)
         T = x.shape[0]
         ws = self.workspace(T, flags)
         if y is None:
             y = torch.empty((T, self.d), dtype=torch.float32, device=self.device)
-        layer_from_x(self.desc(flags), self.weights, w_router, x, bias, logits, y, ws, stream)
+        layer_from_x(self.desc(flags), self.weights, w_router, x, bias, logits, y, ws)
         v = self.views(ws, T, flags)
         return LayerOutput(y=y, **v)
+
+    def _forward_on(self, stream, T: int, y, flags: int, call) -> LayerOutput:
+        caller = torch.cuda.current_stream(self.device)
+        with _on_stream(stream, self.device):
+            out = call()
+        if y is None:  # of the stream's memory, and the caller's to read, as the views are
+            out.y.record_stream(caller)
+        self.workspace(T, flags)
+        return out
