@@ -307,27 +307,29 @@ class Layer:
         self.E, self.f, self.d = gate.E, gate.N, gate.K
         self._buffers = {}
         self._used_on = {}  # handles of the streams that may use each set
+        self._uncleared = set()
 
     def buffers(self, T: int, dtype: torch.dtype) -> dict:
         """The buffers of calls of T tokens of a type, made on the current stream if new."""
         key = (T, dtype)
         here = _raw_stream(self.gate.q.get_device())
-        if key not in self._buffers:
+        new = key not in self._buffers
+        if new:
             E, k, d, f, R = self.E, self.router.top_k, self.d, self.f, T * self.router.top_k
 
-            def new(shape, dt):
+            def make(shape, dt):
                 return torch.empty(shape, dtype=dt, device=self.gate.q.device)
 
-            b = dict(idx=new((T, k), torch.int32), w=new((T, k), torch.float32),
-                     off=new((E + 1,), torch.int32), perm=new((R,), torch.int32),
-                     pos=new((T, k), torch.int32), xq=new((T, d), torch.float8_e4m3fn),
-                     xs=new((T, blocks(d)), torch.float32),
-                     hq=new((R, f), torch.float8_e4m3fn),
-                     hs=new((R, blocks(f)), torch.float32), o=new((R, d), dtype), shared=None)
+            b = dict(idx=make((T, k), torch.int32), w=make((T, k), torch.float32),
+                     off=make((E + 1,), torch.int32), perm=make((R,), torch.int32),
+                     pos=make((T, k), torch.int32), xq=make((T, d), torch.float8_e4m3fn),
+                     xs=make((T, blocks(d)), torch.float32),
+                     hq=make((R, f), torch.float8_e4m3fn),
+                     hs=make((R, blocks(f)), torch.float32), o=make((R, d), dtype), shared=None)
             if self.shared is not None:
                 fs = self.shared[0].N
-                b.update(shq=new((T, fs), torch.float8_e4m3fn),
-                         shs=new((T, blocks(fs)), torch.float32), shared=new((T, d), dtype))
+                b.update(shq=make((T, fs), torch.float8_e4m3fn),
+                         shs=make((T, blocks(fs)), torch.float32), shared=make((T, d), dtype))
             n = max(group_route_workspace_size(self.router, T), workspace_size(max(R, T)))
             b["ws"] = torch.zeros(n, dtype=torch.uint8, device=self.gate.q.device)
             self._buffers[key] = b
@@ -336,6 +338,7 @@ class Layer:
             moe._used_here(self._used_on[key],
                            [t for t in self._buffers[key].values() if t is not None],
                            self.gate.q.device)
+        moe._cleared(self._buffers[key]["ws"], key, self._uncleared, new)
         return self._buffers[key]
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor,

@@ -203,6 +203,21 @@ def _used_here(used_on: set, tensors, device) -> None:
             t.record_stream(stream)
 
 
+def _cleared(ws: torch.Tensor, key, uncleared: set, new: bool) -> torch.Tensor:
+    """A kept workspace, ready for a call.  One that was made while a graph was being captured
+    is cleared by that graph's replays alone: until a call outside of captures has cleared it,
+    each call does."""
+    capturing = torch.cuda.is_current_stream_capturing()
+    if new:
+        if capturing:
+            uncleared.add(key)
+    elif key in uncleared:
+        ws.zero_()
+        if not capturing:
+            uncleared.discard(key)
+    return ws
+
+
 def _dev_ptr(t: Optional[torch.Tensor], dtype=None, name="tensor"):
     if t is None:
         return None
@@ -525,6 +540,7 @@ class Layer:
                                            _dev_ptr(sc, torch.float16, n + "_s")))
         self._ws = {}
         self._used_on = {}  # handles of the streams that may use each workspace
+        self._uncleared = set()
 
     @classmethod
     def from_host(cls, spec, experts: dict, shared: Optional[dict], device):
@@ -552,13 +568,14 @@ class Layer:
     def workspace(self, T: int, flags=0) -> torch.Tensor:
         """The workspace of calls of T tokens, made on the current stream if new."""
         key = (T, flags & FLAG_DEBUG_TAPS)
-        if key not in self._ws:
+        new = key not in self._ws
+        if new:
             n = workspace_size(self.desc(flags), T)
             self._ws[key] = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.device)
             self._used_on[key] = {torch.cuda.current_stream(self.device).cuda_stream}
         else:
             _used_here(self._used_on[key], (self._ws[key],), self.device)
-        return self._ws[key]
+        return _cleared(self._ws[key], key, self._uncleared, new)
 
     def views(self, ws: torch.Tensor, T: int, flags=0) -> dict:
         """Typed views of the workspace regions (for taps and tests)."""

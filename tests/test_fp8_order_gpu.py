@@ -124,3 +124,30 @@ def test_layer_buffers_outlast_every_stream_that_used_them(fp8):  # noqa: F811
     assert not side.query()
     assert at not in [t.data_ptr() for t in other]
     torch.cuda.synchronize()
+
+
+def test_layer_first_call_inside_a_capture(fp8):  # noqa: F811
+    """A capture only records the clearing of buffers that it makes: calls before its first
+    replay, and other captures, clear them for themselves."""
+    T = 3
+    args = layer_inputs(T)
+    want = make_layer(fp8).forward(*args).y.cpu()
+    layer = make_layer(fp8)
+    one, two = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(one):
+        first = layer.forward(*args).y
+        ws = layer.buffers(T, args[0].dtype)["ws"]
+    with torch.cuda.graph(two):
+        second = layer.forward(*args).y
+    ws.fill_(0x55)  # what the memory may hold
+    two.replay()
+    assert torch.equal(second.cpu(), want) and fp8.check_device_error(ws) == 0
+    ws.fill_(0x55)
+    assert torch.equal(layer.forward(*args).y.cpu(), want) and fp8.check_device_error(ws) == 0
+    assert layer.buffers(T, args[0].dtype)["ws"].data_ptr() == ws.data_ptr()
+    for _ in range(2):
+        first.zero_()
+        one.replay()
+        assert torch.equal(first.cpu(), want)
+        assert torch.equal(layer.forward(*args).y.cpu(), want)
+    assert fp8.check_device_error(ws) == 0

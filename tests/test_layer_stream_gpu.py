@@ -86,3 +86,24 @@ def test_output_outlasts_its_stream(gpu):
     assert at not in [t.data_ptr() for t in other]
     torch.cuda.synchronize()
     assert not any(t.any() for t in other)
+
+
+def test_first_call_inside_a_capture(gpu):
+    """A capture only records the clearing of a workspace that it makes: a call before its
+    first replay clears it for itself."""
+    from routed_expert_decode_gb300 import moe
+
+    args = inputs(9, gpu)
+    want = fresh_layer(gpu).forward(*args).y.cpu()
+    layer, graph = fresh_layer(gpu), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = layer.forward(*args).y
+        ws = layer.workspace(9)
+    ws[:1 << 14].fill_(0x55)  # what the memory may hold
+    assert torch.equal(layer.forward(*args).y.cpu(), want) and moe.check_device_error(ws) == 0
+    for _ in range(2):
+        y.zero_()
+        graph.replay()
+        assert torch.equal(y.cpu(), want)
+        assert torch.equal(layer.forward(*args).y.cpu(), want)
+    assert moe.check_device_error(ws) == 0
