@@ -266,8 +266,8 @@ def combine(o, w, pos, y, shared=None, stream=None) -> None:
 # ------------------------------------------------------------------ convenience
 @dataclass
 class LayerOutput:
-    """What a layer call computed: its result and the buffers it went through (valid
-    until the layer's next call with as many tokens)."""
+    """What a layer call computed: its result and the buffers it went through (their
+    values are valid until the layer's next call with as many tokens)."""
     y: torch.Tensor
     idx: torch.Tensor
     w: torch.Tensor
@@ -288,11 +288,13 @@ class Layer:
 
     ``gate``, ``up`` [E, f, d] and ``down`` [E, d, f] are ``Mat``; ``shared`` is a
     triple of one-expert ``Mat`` or None.  Buffers and the workspace are kept per number
-    of tokens and type, as ``moe.Layer`` keeps its own; calls that overlap need layers
-    (or streams' orders) of their own.  What a call makes, it makes on its stream.
+    of tokens and type, the last used up to ``keep_bytes`` in all (and those that a
+    captured graph uses: its replays need them); calls that overlap need layers (or
+    streams' orders) of their own.  What a call makes, it makes on its stream.
     """
 
-    def __init__(self, router: MoeRouter, gate: Mat, up: Mat, down: Mat, shared=None):
+    def __init__(self, router: MoeRouter, gate: Mat, up: Mat, down: Mat, shared=None,
+                 keep_bytes: int = 4 << 30):
         if (gate.E, gate.N, gate.K) != (up.E, up.N, up.K) or \
                 (down.E, down.N, down.K) != (gate.E, gate.K, gate.N) or \
                 router.n_expert != gate.E:
@@ -305,7 +307,9 @@ class Layer:
                 raise ValueError("shared must be (gate, up, down) of one expert")
         self.router, self.gate, self.up, self.down, self.shared = router, gate, up, down, shared
         self.E, self.f, self.d = gate.E, gate.N, gate.K
-        self._buffers = {}
+        self.keep_bytes = keep_bytes
+        self._buffers = {}  # the last used at the end
+        self._bytes = {}    # of each set that may be dropped
         self._used_on = {}  # handles of the streams that may use each set
         self._uncleared = set()
 
@@ -332,14 +336,30 @@ class Layer:
                          shs=make((T, blocks(fs)), torch.float32), shared=make((T, d), dtype))
             n = max(group_route_workspace_size(self.router, T), workspace_size(max(R, T)))
             b["ws"] = torch.zeros(n, dtype=torch.uint8, device=self.gate.q.device)
-            self._buffers[key] = b
+            self._bytes[key] = sum(t.numel() * t.element_size() for t in b.values()
+                                   if t is not None)
             self._used_on[key] = {here}
-        elif here not in self._used_on[key]:
-            moe._used_here(self._used_on[key],
-                           [t for t in self._buffers[key].values() if t is not None],
-                           self.gate.q.device)
-        moe._cleared(self._buffers[key]["ws"], key, self._uncleared, new)
-        return self._buffers[key]
+        else:
+            b = self._buffers.pop(key)
+            if here not in self._used_on[key]:
+                moe._used_here(self._used_on[key], [t for t in b.values() if t is not None],
+                               self.gate.q.device)
+        self._buffers[key] = b
+        moe._cleared(b["ws"], key, self._uncleared, new)
+        if torch.cuda.is_current_stream_capturing():
+            self._bytes.pop(key, None)
+        if new:
+            self._drop_unused(key)
+        return b
+
+    def _drop_unused(self, key) -> None:
+        """Forget the sets that were not used for longest, down to keep_bytes (never ``key``)."""
+        total = sum(self._bytes.values())
+        for old in [k for k in self._buffers if k in self._bytes and k != key]:
+            if total <= self.keep_bytes:
+                break
+            total -= self._bytes.pop(old)
+            del self._buffers[old], self._used_on[old]
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor,
                 bias: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,

@@ -151,3 +151,42 @@ def test_layer_first_call_inside_a_capture(fp8):  # noqa: F811
         assert torch.equal(first.cpu(), want)
         assert torch.equal(layer.forward(*args).y.cpu(), want)
     assert fp8.check_device_error(ws) == 0
+
+
+def test_layer_memory_is_bounded(fp8):  # noqa: F811
+    """Buffers of the least recently used token counts are dropped; results, outputs in hand
+    and captured graphs do not notice."""
+    def size(b):
+        return sum(t.numel() * t.element_size() for t in b.values() if t is not None)
+
+    big = size(make_layer(fp8).buffers(200, torch.bfloat16))
+    layer = make_layer(fp8, keep_bytes=3 * big)
+    want = {T: make_layer(fp8).forward(*layer_inputs(T)).y.cpu() for T in range(190, 201)}
+    args = {T: layer_inputs(T) for T in want}
+    graph = torch.cuda.CUDAGraph()
+    layer.forward(*args[190])
+    with torch.cuda.graph(graph):
+        y = layer.forward(*args[190]).y
+    kept = layer.buffers(190, torch.bfloat16)
+    held = layer.forward(*args[191])
+    idx = held.idx.clone()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        for T in sorted(want):
+            out = layer.forward(*args[T])
+            assert torch.equal(out.y.cpu(), want[T])
+            assert layer.buffers(T, torch.bfloat16)["o"].data_ptr() == out.o.data_ptr()
+            del out
+            sets = layer._buffers
+            assert sum(size(b) for k, b in sets.items() if k[0] != 190) <= 3 * big
+            assert set(sets) == set(layer._used_on)
+        y.zero_()
+        graph.replay()
+        assert torch.equal(y.cpu(), want[190])
+    assert layer.buffers(190, torch.bfloat16) is kept
+    assert torch.equal(held.idx, idx) and torch.equal(held.y.cpu(), want[191])
+    # a set larger than the limit still serves its own calls
+    small = make_layer(fp8, keep_bytes=0)
+    for T in (190, 191, 190):
+        assert torch.equal(small.forward(*args[T]).y.cpu(), want[T])
+        assert len(small._buffers) == 1
