@@ -3,7 +3,8 @@
 Argument marshalling only, as ``moe``: every operator runs in the library's CUDA
 kernels on the caller's tensors and stream, and a bad argument raises
 ``MoeError`` (or ``ValueError`` for a tensor of another device, type or shape)
-before anything is enqueued.
+before anything is enqueued.  A call runs on the device of its tensors, which is all of
+theirs and its stream's, whether or not it is the current one.
 
 Entry points mirror the C names: ``group_route``, ``quantize``, ``swiglu``,
 ``product``, ``combine``.  A row tensor may have any row stride, its columns are
@@ -53,8 +54,9 @@ _lib = None
 
 def lib():
     """The library with this header's signatures (loaded once; raises if absent)."""
-    global _lib
+    global _lib, _many
     if _lib is None:
+        _many = torch.cuda.device_count() > 1
         L = moe.lib()
         _pr, _pm, _px = (ctypes.POINTER(t) for t in (MoeRouter, Fp8Mat, Fp8Rows))
         L.moe_group_route_workspace_size.restype = _sz
@@ -88,20 +90,35 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _stream(stream, t: torch.Tensor):
-    """Handle of ``stream``, or of the current stream of t's device."""
-    return _raw_stream(t.get_device()) if stream is None else moe._stream(stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_many = True  # whether there may be devices other than the current one (0.3 us a call)
 
 
-def _rows2d(t: torch.Tensor, cols: int, name: str):
-    """(pointer, dtype code, row stride) of a 2-d CUDA tensor with consecutive columns, which
-    number ``cols``."""
+def _elsewhere(dev: int, call, *args) -> None:
+    """``call`` with device ``dev``, which is not the current one, made current: the library
+    launches on the current device.  -1 is no CUDA device."""
+    if dev < 0:
+        raise ValueError(f"{call.__name__} needs CUDA tensors")
+    with torch.cuda.device(dev):
+        call(*args)
+
+
+def _stream(stream, dev: int):
+    """Handle of ``stream``, which must be of device ``dev``."""
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+        raise ValueError(f"stream must be of cuda:{dev}, got one of {stream.device}")
+    return moe._stream(stream)
+
+
+def _rows2d(t: torch.Tensor, cols: int, name: str, dev: int):
+    """(pointer, dtype code, row stride) of a 2-d tensor on device ``dev`` with consecutive
+    columns, which number ``cols``."""
     dt = DTYPES.get(t.dtype)
     ld, step = t.stride()
-    if dt is None or step != 1 or ld < cols or not t.is_cuda:
+    if dt is None or step != 1 or ld < cols or t.get_device() != dev:
         rows = t.shape[0]
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
         if dt is None:
             raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
         if step != 1 and cols > 1:
@@ -113,12 +130,12 @@ def _rows2d(t: torch.Tensor, cols: int, name: str):
     return t.data_ptr(), dt, ld
 
 
-def _plane(t: torch.Tensor, dtypes, shape, name: str) -> int:
-    """Pointer of a contiguous CUDA tensor of one of the dtypes and this shape."""
-    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.is_cuda:
+def _plane(t: torch.Tensor, dtypes, shape, name: str, dev: int) -> int:
+    """Pointer of a contiguous tensor on device ``dev`` of one of the dtypes and this shape."""
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
         return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtypes[0]} and shape "
-                     f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    raise ValueError(f"{name} must be a contiguous tensor of {dtypes[0]} and shape "
+                     f"{tuple(shape)} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 _CODES = (torch.float8_e4m3fn, torch.uint8)
@@ -126,11 +143,11 @@ _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 
 
-def _ws(ws: torch.Tensor):
-    if ws.dtype is torch.uint8 and ws.is_contiguous() and ws.is_cuda:
+def _ws(ws: torch.Tensor, dev: int):
+    if ws.dtype is torch.uint8 and ws.is_contiguous() and ws.get_device() == dev:
         return ws.data_ptr(), ws.numel()
-    raise ValueError(f"ws must be a contiguous CUDA tensor of torch.uint8, got {ws.dtype} on "
-                     f"{ws.device}")
+    raise ValueError(f"ws must be a contiguous tensor of torch.uint8 on cuda:{dev}, got {ws.dtype} "
+                     f"on {ws.device}")
 
 
 # ------------------------------------------------------------------ router
@@ -149,18 +166,23 @@ def group_route(router: MoeRouter, logits, bias: Optional[torch.Tensor], idx, w,
                 ws, stream=None) -> None:
     """moe_group_route: picks and weights of ``logits`` [T, E] (float32, bfloat16 or
     float16), and the stable row permutation by expert."""
+    dev = logits.get_device()
+    if dev < 0 or _many and dev != _current_device():
+        return _elsewhere(dev, group_route, router, logits, bias, idx, w, off, perm, pos, ws,
+                          stream)
     T, E = logits.shape
     k = router.top_k
     if E != router.n_expert:
         raise ValueError(f"logits must have {router.n_expert} columns, got {E}")
-    lp, dt, ld = _rows2d(logits, E, "logits")
-    wsp, wsn = _ws(ws)
+    lp, dt, ld = _rows2d(logits, E, "logits", dev)
+    wsp, wsn = _ws(ws, dev)
     st = (_lib or lib()).moe_group_route(
         ctypes.byref(router), lp, dt, ld,
-        None if bias is None else _plane(bias, _F32, (E,), "bias"), T,
-        _plane(idx, _I32, (T, k), "idx"), _plane(w, _F32, (T, k), "w"),
-        _plane(off, _I32, (E + 1,), "off"), _plane(perm, _I32, (T * k,), "perm"),
-        _plane(pos, _I32, (T, k), "pos"), wsp, wsn, _stream(stream, logits))
+        None if bias is None else _plane(bias, _F32, (E,), "bias", dev), T,
+        _plane(idx, _I32, (T, k), "idx", dev), _plane(w, _F32, (T, k), "w", dev),
+        _plane(off, _I32, (E + 1,), "off", dev), _plane(perm, _I32, (T * k,), "perm", dev),
+        _plane(pos, _I32, (T, k), "pos", dev), wsp, wsn,
+        _raw_stream(dev) if stream is None else _stream(stream, dev))
     if st:
         _check("moe_group_route", st)
 
@@ -169,11 +191,14 @@ def group_route(router: MoeRouter, logits, bias: Optional[torch.Tensor], idx, w,
 def quantize(x, q, scale, stream=None) -> None:
     """moe_fp8_quantize: rows of ``x`` [T, d] to e4m3 codes ``q`` [T, d] and fp32
     scales ``scale`` [T, ceil(d / 128)]."""
+    dev = x.get_device()
+    if dev < 0 or _many and dev != _current_device():
+        return _elsewhere(dev, quantize, x, q, scale, stream)
     T, d = x.shape
-    xp, dt, ld = _rows2d(x, d, "x")
-    st = (_lib or lib()).moe_fp8_quantize(xp, dt, ld, T, d, _plane(q, _CODES, (T, d), "q"),
-                                _plane(scale, _F32, (T, blocks(d)), "scale"),
-                                _stream(stream, x))
+    xp, dt, ld = _rows2d(x, d, "x", dev)
+    st = (_lib or lib()).moe_fp8_quantize(xp, dt, ld, T, d, _plane(q, _CODES, (T, d), "q", dev),
+                                _plane(scale, _F32, (T, blocks(d)), "scale", dev),
+                                _raw_stream(dev) if stream is None else _stream(stream, dev))
     if st:
         _check("moe_fp8_quantize", st)
 
@@ -188,8 +213,12 @@ class Mat:
             q, scale = q[None], scale[None]
         self.E, self.N, self.K = q.shape
         self.q, self.scale = q, scale
-        self.c = Fp8Mat(_plane(q, _CODES, q.shape, "q"),
-                        _plane(scale, _F32, (self.E, blocks(self.N), blocks(self.K)), "scale"))
+        self.dev = q.get_device()
+        if self.dev < 0:
+            raise ValueError(f"q must be a CUDA tensor, got one on {q.device}")
+        self.c = Fp8Mat(_plane(q, _CODES, q.shape, "q", self.dev),
+                        _plane(scale, _F32, (self.E, blocks(self.N), blocks(self.K)), "scale",
+                               self.dev))
         self.ref = ctypes.byref(self.c)
 
 
@@ -198,12 +227,14 @@ def workspace_size(rows: int) -> int:
     return int(lib().moe_fp8_workspace_size(rows))
 
 
-def _activation(w: Mat, xq, xs, rows: int, off, perm, top_k: int):
+def _activation(w: Mat, xq, xs, rows: int, off, perm, top_k: int, dev: int):
     n = xq.shape[0]
-    return Fp8Rows(_plane(xq, _CODES, (n, w.K), "xq"),
-                   _plane(xs, _F32, (n, blocks(w.K)), "xs"), n, rows,
-                   None if off is None else _plane(off, _I32, (w.E + 1,), "off"),
-                   None if perm is None else _plane(perm, _I32, (rows,), "perm"), top_k)
+    if w.dev != dev:
+        raise ValueError(f"the weights must be on cuda:{dev}, got cuda:{w.dev}")
+    return Fp8Rows(_plane(xq, _CODES, (n, w.K), "xq", dev),
+                   _plane(xs, _F32, (n, blocks(w.K)), "xs", dev), n, rows,
+                   None if off is None else _plane(off, _I32, (w.E + 1,), "off", dev),
+                   None if perm is None else _plane(perm, _I32, (rows,), "perm", dev), top_k)
 
 
 def product(w: Mat, xq, xs, out, ws, off=None, perm=None, top_k: int = 1, stream=None) -> None:
@@ -211,14 +242,17 @@ def product(w: Mat, xq, xs, out, ws, off=None, perm=None, top_k: int = 1, stream
     weights, transposed.  ``off`` [E + 1] gives each expert's rows (None: one
     expert, all rows); ``perm`` [R] with ``top_k`` makes row r read activation row
     perm[r] // top_k (None: row r)."""
+    dev = out.get_device()
+    if dev < 0 or _many and dev != _current_device():
+        return _elsewhere(dev, product, w, xq, xs, out, ws, off, perm, top_k, stream)
     R, N = out.shape
     if N != w.N:
         raise ValueError(f"out must have {w.N} columns, got {N}")
-    op, dt, ld = _rows2d(out, N, "out")
-    x = _activation(w, xq, xs, R, off, perm, top_k)
-    wsp, wsn = _ws(ws)
+    op, dt, ld = _rows2d(out, N, "out", dev)
+    x = _activation(w, xq, xs, R, off, perm, top_k, dev)
+    wsp, wsn = _ws(ws, dev)
     st = (_lib or lib()).moe_fp8_product(w.ref, w.E, N, w.K, ctypes.byref(x), op, dt, ld, wsp, wsn,
-                               _stream(stream, out))
+                               _raw_stream(dev) if stream is None else _stream(stream, dev))
     if st:
         _check("moe_fp8_product", st)
 
@@ -227,15 +261,18 @@ def swiglu(gate: Mat, up: Mat, xq, xs, hq, hs, ws, off=None, perm=None, top_k: i
            stream=None) -> None:
     """moe_fp8_swiglu: ``hq`` [R, f], ``hs`` [R, ceil(f / 128)] = silu(x Wg) * (x Wu),
     quantised; rows as in ``product``."""
+    dev = hq.get_device()
+    if dev < 0 or _many and dev != _current_device():
+        return _elsewhere(dev, swiglu, gate, up, xq, xs, hq, hs, ws, off, perm, top_k, stream)
     R = hq.shape[0]
-    if (up.E, up.N, up.K) != (gate.E, gate.N, gate.K):
-        raise ValueError("gate and up must have the same shape")
-    x = _activation(gate, xq, xs, R, off, perm, top_k)
-    wsp, wsn = _ws(ws)
+    if (up.E, up.N, up.K, up.dev) != (gate.E, gate.N, gate.K, gate.dev):
+        raise ValueError("gate and up must have the same shape and device")
+    x = _activation(gate, xq, xs, R, off, perm, top_k, dev)
+    wsp, wsn = _ws(ws, dev)
     st = (_lib or lib()).moe_fp8_swiglu(gate.ref, up.ref, gate.E, gate.N, gate.K, ctypes.byref(x),
-                              _plane(hq, _CODES, (R, gate.N), "hq"),
-                              _plane(hs, _F32, (R, blocks(gate.N)), "hs"), wsp, wsn,
-                              _stream(stream, hq))
+                              _plane(hq, _CODES, (R, gate.N), "hq", dev),
+                              _plane(hs, _F32, (R, blocks(gate.N)), "hs", dev), wsp, wsn,
+                              _raw_stream(dev) if stream is None else _stream(stream, dev))
     if st:
         _check("moe_fp8_swiglu", st)
 
@@ -244,21 +281,24 @@ def swiglu(gate: Mat, up: Mat, xq, xs, hq, hs, ws, off=None, perm=None, top_k: i
 def combine(o, w, pos, y, shared=None, stream=None) -> None:
     """moe_fp8_combine: ``y`` [T, d] = ``shared`` [T, d] + sum over slots j of
     ``w`` [T, k] * ``o`` [R, d] at row ``pos`` [T, k]."""
+    dev = y.get_device()
+    if dev < 0 or _many and dev != _current_device():
+        return _elsewhere(dev, combine, o, w, pos, y, shared, stream)
     T, d = y.shape
     R, do = o.shape
     k = pos.shape[1]
     if do != d or (shared is not None and shared.shape != (T, d)):
         raise ValueError(f"o and shared must have {d} columns, shared {T} rows")
-    op, dt, ldo = _rows2d(o, d, "o")
-    yp, ydt, ldy = _rows2d(y, d, "y")
+    op, dt, ldo = _rows2d(o, d, "o", dev)
+    yp, ydt, ldy = _rows2d(y, d, "y", dev)
     sp, lds = None, 0
     if shared is not None:
-        sp, sdt, lds = _rows2d(shared, d, "shared")
+        sp, sdt, lds = _rows2d(shared, d, "shared", dev)
         if sdt != dt:
             raise ValueError("shared must have o's type")
-    st = (_lib or lib()).moe_fp8_combine(op, dt, ldo, R, _plane(w, _F32, (T, k), "w"),
-                               _plane(pos, _I32, (T, k), "pos"), T, k, d, sp, lds, yp, ydt, ldy,
-                               _stream(stream, y))
+    st = (_lib or lib()).moe_fp8_combine(op, dt, ldo, R, _plane(w, _F32, (T, k), "w", dev),
+                               _plane(pos, _I32, (T, k), "pos", dev), T, k, d, sp, lds, yp, ydt,
+                               ldy, _raw_stream(dev) if stream is None else _stream(stream, dev))
     if st:
         _check("moe_fp8_combine", st)
 
@@ -295,6 +335,8 @@ class Layer:
 
     def __init__(self, router: MoeRouter, gate: Mat, up: Mat, down: Mat, shared=None,
                  keep_bytes: int = 4 << 30):
+        if len({m.dev for m in (gate, up, down, *(shared or ()))}) > 1:
+            raise ValueError("the weights must be on one device")
         if (gate.E, gate.N, gate.K) != (up.E, up.N, up.K) or \
                 (down.E, down.N, down.K) != (gate.E, gate.K, gate.N) or \
                 router.n_expert != gate.E:
@@ -316,7 +358,7 @@ class Layer:
     def buffers(self, T: int, dtype: torch.dtype) -> dict:
         """The buffers of calls of T tokens of a type, made on the current stream if new."""
         key = (T, dtype)
-        here = _raw_stream(self.gate.q.get_device())
+        here = _raw_stream(self.gate.dev)
         new = key not in self._buffers
         if new:
             E, k, d, f, R = self.E, self.router.top_k, self.d, self.f, T * self.router.top_k
@@ -367,6 +409,7 @@ class Layer:
         """y [T, d] of x [T, d] and its router logits [T, E]; y has x's type unless given.  With a
         ``stream`` the whole call runs there, and what it makes belongs to it."""
         if stream is not None:
+            _stream(stream, self.gate.dev)  # refuses another device's
             caller = torch.cuda.current_stream(self.gate.q.device)
             with moe._on_stream(stream, self.gate.q.device):
                 out = self.forward(x, logits, bias, y)
@@ -374,6 +417,9 @@ class Layer:
                 out.y.record_stream(caller)
             self.buffers(x.shape[0], x.dtype)
             return out
+        if _many and self.gate.dev != _current_device():
+            with torch.cuda.device(self.gate.dev):
+                return self.forward(x, logits, bias, y)
         T = x.shape[0]
         k = self.router.top_k
         b = self.buffers(T, x.dtype)
