@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include "fp8_host.h"
 #include "moe_fp8.h"
 #include "moe_internal.cuh"
 
@@ -140,35 +141,19 @@ __device__ __forceinline__ void fp8_block_scale(float amax, float &scale, float 
 }
 
 // ---------------------------------------------------------------- launchers
-constexpr int kMaxDevices = 64;
-// the current device, -1 when there is none (or it is past kMaxDevices)
-inline int device_here() {
-  int dev = -1;
-  return cudaGetDevice(&dev) == cudaSuccess && dev < kMaxDevices ? dev : -1;
-}
 // CTAs of a kernel that runs one per SM (a device's SM count is looked up once)
 inline int fp8_ctas() {
-  static int known[kMaxDevices];
+  static std::atomic<int> known[kMaxDevices];
   const int dev = device_here();
   if (dev < 0) return kSmCount;
-  if (known[dev] == 0) {
-    int n = 0;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
       return kSmCount;
-    known[dev] = n < (int)kFp8MaxCtas ? n : (int)kFp8MaxCtas;
+    n = n < (int)kFp8MaxCtas ? n : (int)kFp8MaxCtas;
+    known[dev].store(n, std::memory_order_relaxed);
   }
-  return known[dev];
-}
-// allow `kern` that much dynamic shared memory on the current device; the largest
-// size so far is kept per kernel and device (`set`: kMaxDevices zeros of the caller)
-template <typename K>
-cudaError_t allow_smem(K kern, size_t smem, int *set) {
-  const int dev = device_here();
-  if (dev >= 0 && (int)smem <= set[dev]) return cudaSuccess;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess && dev >= 0) set[dev] = (int)smem;
-  return e;
+  return n;
 }
 cudaError_t launch_fp8_quantize(const void *x, int dt, size_t ld, uint32_t T, uint32_t d, void *q,
                                 float *scale, cudaStream_t stream);

@@ -131,8 +131,8 @@ cudaError_t run_core(Fp8Args &a, cudaStream_t stream) {
   fp8_set_tiles(a, fp8_blocks(a.N), 1);
   const size_t smem = 4 * ((size_t)(kCoreM + (SWIGLU ? 2 : 1) * kCoreN) * (kCoreSlab + 1)) +
                       fp8_tiles_smem(a.E);
-  static int set[kMaxDevices];
-  const cudaError_t e = allow_smem(kern, smem, set);
+  static std::atomic<bool> done[kMaxDevices];
+  const cudaError_t e = allow_smem(kern, done);
   if (e != cudaSuccess) return e;
   return launch_k(kern, 4 * fp8_ctas(), kCoreThreads, smem, stream, true, a);
 }

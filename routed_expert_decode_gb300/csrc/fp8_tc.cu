@@ -501,8 +501,8 @@ cudaError_t run_tc(Fp8Args &a, cudaStream_t stream) {
   int ns = (int)((kSmemLimit - rest) / kStage);
   if (ns > (int)kTcStages) ns = kTcStages;
   const size_t smem = rest + ns * (size_t)kStage;
-  static int set[kMaxDevices];
-  const cudaError_t e = allow_smem(kern, smem, set);
+  static std::atomic<bool> done[kMaxDevices];
+  const cudaError_t e = allow_smem(kern, done);
   if (e != cudaSuccess) return e;
   return launch_k(kern, sms, kTcThreads, smem, stream, true, a, maps, (uint32_t)ns, vec);
 }

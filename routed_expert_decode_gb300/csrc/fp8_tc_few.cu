@@ -449,8 +449,8 @@ cudaError_t run_few(Fp8Args &a, cudaStream_t stream) {
   int ns = (int)((kSmemLimit - rest) / stage);
   if (ns > kMaxStages) ns = kMaxStages;
   const size_t smem = rest + ns * stage;
-  static int set[kMaxDevices];
-  const cudaError_t e = allow_smem(kern, smem, set);
+  static std::atomic<bool> done[kMaxDevices];
+  const cudaError_t e = allow_smem(kern, done);
   if (e != cudaSuccess) return e;
   // Tiles are split along K when they leave three SMs of four idle and K has 16 blocks:
   // 64 SMs already draw 5.4 TB/s, and under a saturated HBM each of the split's round

@@ -14,7 +14,6 @@ constexpr int kMinShare = 4;             // K blocks a CTA takes of a split roun
 constexpr long long kWaitCycles = 4000000000ll;  // ~2 s
 constexpr int kSpin = 1 << 26;
 constexpr int kHintNs = 20000;  // try_wait suspend-time hint: waiting warps sleep, not spin
-constexpr size_t kSmemLimit = 232448;  // shared memory of a CTA
 
 // ---------------------------------------------------------------- PTX helpers
 __device__ __forceinline__ uint32_t s32(const void *p) {
