@@ -178,9 +178,12 @@ __device__ __forceinline__ void fp8_store(const Fp8Args &a, int r, uint32_t n, f
   else ((__half *)a.out)[i] = __float2half_rn(v);
 }
 
-// h = g / (1 + e^-g) * u
+// h = g / (1 + e^-g) * u.  __fdividef gives 0 for divisors above 2^126 (g of -87.4 to
+// -88.7): both sides of a large one are scaled down, which changes no quotient.
 __device__ __forceinline__ float fp8_swiglu_value(float g, float u) {
-  return __fdividef(g, 1.0f + __expf(-g)) * u;
+  const float d = 1.0f + __expf(-g);
+  const float t = d > 0x1p100f ? 0x1p-64f : 1.0f;
+  return __fdividef(g * t, d * t) * u;
 }
 
 }  // namespace moe
