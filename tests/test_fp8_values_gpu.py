@@ -41,3 +41,57 @@ def test_swiglu_of_large_negative_gates(fp8, T, K):  # noqa: F811
     fp8.swiglu(gate, up, dev(xq), dev(xs), hq, hs, ws)
     assert fp8.check_device_error(ws) == 0
     check_h(hq, hs, g, np.zeros_like(g), u, eu)
+
+
+def any_codes(rng, shape):
+    """Random codes but NaN's."""
+    q = rng.integers(0, 256, shape, dtype=np.uint8)
+    q[(q & 0x7F) == 0x7F] &= 0xF8
+    return q
+
+
+SHARED_CASES = [
+    # T, E, k, N, the experts that rows go to: few tiles (or few over a whole round), which are
+    # shared along K.  Tiles of 32 rows by one block of columns,
+    (1, 1, 1, 1000, 1),
+    (5, 4, 2, 300, 4),
+    (31, 2, 1, 130, 2),
+    # by two,
+    (12, 24, 2, 1000, 3),
+    (30, 40, 1, 500, 2),
+    # by two, beyond a round of whole tiles on every SM,
+    (80, 160, 8, 136, 160),
+    # and of 64 rows, their second half ragged, full or empty
+    (55, 1, 1, 300, 1),
+    (64, 1, 1, 130, 1),
+    (90, 1, 1, 520, 1),
+    (110, 2, 1, 264, 2),
+]
+
+
+@pytest.mark.parametrize("K", [2064, 6160])
+@pytest.mark.parametrize("T,E,k,N,live", SHARED_CASES)
+def test_product_of_few_rows_shared_along_k(fp8, T, E, k, N, live, K):  # noqa: F811
+    if E * N * K > 1 << 26:
+        K = 2048
+    rng = np.random.default_rng(T * 13 + E + N)
+    off, perm, _ = assignment(rng, T, E, k, empty=range(live, E))
+    q = any_codes(rng, (E, N, K))
+    s = ((0.5 + rng.random((E, ref.nb(N), ref.nb(K)))) / (100 * np.sqrt(K))).astype(np.float32)
+    w, R = fp8.Mat(dev(q), dev(s)), T * k
+    ws = workspace(fp8, R)
+    for gathered in (True, False):
+        xq = any_codes(rng, (T if gathered else R, K))
+        xs = ((0.5 + rng.random((len(xq), ref.nb(K)))) / 100).astype(np.float32)
+        xrow = perm // k if gathered else np.arange(R)
+        y, e = expected(ref.dequantize(xq, xs), off, xrow, q, s, R, N)
+        args = dict(off=dev(off), perm=dev(perm) if gathered else None, top_k=k)
+        for dt, t in (("f32", torch.float32), ("bf16", torch.bfloat16)):
+            outs = []
+            for _ in range(2):
+                out = torch.full((R, N), float("nan"), dtype=t, device="cuda")
+                fp8.product(w, dev(xq), dev(xs), out, ws, **args)
+                outs.append(out)
+            check_out(outs[0], y, e, dt)
+            assert torch.equal(*outs)
+    assert fp8.check_device_error(ws) == 0
