@@ -66,6 +66,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<uint32_t *>(&r);
 }
 
+// v / d with inv = floor((2^32 - 1) / d): the product's high word is at most one short
+__device__ __forceinline__ uint32_t quotient(uint32_t v, uint32_t d, uint32_t inv) {
+  const uint32_t q = __umulhi(v, inv);
+  return v - q * d >= d ? q + 1 : q;
+}
+
 // 16 bytes, read once (no L1 allocation).  Volatile, and not a read-only load:
 // a load of what the stream's previous kernel wrote must stay behind pdl_wait
 __device__ __forceinline__ uint4 ld_once16(const void *p) {

@@ -173,16 +173,13 @@ __device__ __forceinline__ void tc_ld32(uint32_t taddr, float (&v)[32]) {
       : "r"(taddr));
 }
 // waits for the warp's loads; the registers of v pass through it so that no use of
-// them can move above the wait (tie32: the same for a second load)
+// them can move above the wait
 __device__ __forceinline__ void tc_wait_ld32(float (&v)[32]) {
 #define R4(i) "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3])
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : R4(0), R4(4), R4(8), R4(12), R4(16), R4(20), R4(24), R4(28)::"memory");
 }
-__device__ __forceinline__ void tie32(float (&v)[32]) {
-  asm volatile("" : R4(0), R4(4), R4(8), R4(12), R4(16), R4(20), R4(24), R4(28));
 #undef R4
-}
 __device__ __forceinline__ void st_global32(void *p, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
                "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])

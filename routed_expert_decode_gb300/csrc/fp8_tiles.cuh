@@ -7,8 +7,6 @@
 
 namespace moe {
 
-constexpr uint32_t kFp8MaxExperts = 1024;
-
 // arguments shared by the product kernels
 struct Fp8Args {
   uint32_t E, N, K, nbn, nbk;  // nbn, nbk: blocks of 128 along N and K
@@ -130,12 +128,6 @@ __device__ __forceinline__ RowTiles fp8_row_tiles(const Fp8Args &a, int *sm) {
 struct Fp8Tile {
   int e, row0, rows, nt;  // expert, first output row, live rows, column tile
 };
-
-// v / d with inv = floor((2^32 - 1) / d): the product's high word is at most one short
-__device__ __forceinline__ uint32_t quotient(uint32_t v, uint32_t d, uint32_t inv) {
-  const uint32_t q = __umulhi(v, inv);
-  return v - q * d >= d ? q + 1 : q;
-}
 
 // By a whole warp: tile v of total * n_tiles: experts in order, an expert's column tiles one
 // after another, its row tiles innermost (they share the weights)

@@ -64,12 +64,6 @@ struct GrArgs {
   uint32_t per, per_inv;  // tokens of a run, floor((2^32 - 1) / per)
 };
 
-// v / d with inv = floor((2^32 - 1) / d): the product's high word is at most one short
-__device__ __forceinline__ uint32_t quot(uint32_t v, uint32_t d, uint32_t inv) {
-  const uint32_t q = __umulhi(v, inv);
-  return v - q * d >= d ? q + 1 : q;
-}
-
 // The arguments into the constant cache before the wait for earlier work: a
 // launch's are always cold, and the first uses come one after another.
 __device__ __forceinline__ void gr_warm(const GrArgs &a) {
@@ -276,7 +270,7 @@ __device__ __forceinline__ void route_token(const GrArgs &a, uint32_t t, int lan
   if (slot) {
     a.idx[(size_t)t * k + lane] = mine;
     a.w[(size_t)t * k + lane] = w;
-    if (a.hist) atomicAdd(a.hist + (size_t)quot(t, a.per, a.per_inv) * E + mine, 1);
+    if (a.hist) atomicAdd(a.hist + (size_t)quotient(t, a.per, a.per_inv) * E + mine, 1);
   }
 }
 
@@ -325,7 +319,7 @@ __global__ void __launch_bounds__(kPlaceThreads) k_group_place(const PlaceArgs a
     const int32_t *p = a.idx + (size_t)x * k;
     for (uint32_t i = tid; i < n; i += kPlaceThreads) use(p[i], i);
   };
-  auto token_of = [&](uint32_t i) { return quot(i, k, a.k_inv); };
+  auto token_of = [&](uint32_t i) { return quotient(i, k, a.k_inv); };
   int all = 0, ahead = 0;  // thread e: rows of expert e, and those of earlier CTAs
   if (gridDim.x == 1) {
     each(t0, t1, [&](int e, uint32_t) { atomicAdd(&count[e], 1); });
