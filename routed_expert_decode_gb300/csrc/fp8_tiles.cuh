@@ -170,12 +170,16 @@ __device__ __forceinline__ void fp8_store(const Fp8Args &a, int r, uint32_t n, f
   else ((__half *)a.out)[i] = __float2half_rn(v);
 }
 
-// h = g / (1 + e^-g) * u.  __fdividef gives 0 for divisors above 2^126 (g of -87.4 to
-// -88.7): both sides of a large one are scaled down, which changes no quotient.
+// h = g / (1 + e^-g) * u, with the special function unit's 2^x and 1 / x (2 ulp each).
+// Its 1 / x of more than 2^126 (g of -87.4 to -88.7) would be a subnormal, which it
+// flushes to 0: a quarter of the divisor never is that large, and a quarter of both
+// sides is the same quotient.  A flushed e^-g is nothing beside 1.
 __device__ __forceinline__ float fp8_swiglu_value(float g, float u) {
-  const float d = 1.0f + __expf(-g);
-  const float t = d > 0x1p100f ? 0x1p-64f : 1.0f;
-  return __fdividef(g * t, d * t) * u;
+  constexpr float kLog2E = 1.4426950408889634f;
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-kLog2E * g));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fmaf_rn(e, 0.25f, 0.25f)));
+  return 0.25f * g * r * u;
 }
 
 }  // namespace moe
