@@ -15,7 +15,8 @@ constexpr uint32_t kQuantSpan = 4 * kQuantSteps;  // blocks per warp: four a ste
 // maximum is three shuffles and a lane's codes are one 16-byte store; a warp takes
 // 8 consecutive blocks of one row with all its loads issued first (64 bytes a lane
 // of a 16-bit type).  VEC: rows whose blocks are whole and 16-byte aligned.  8192 rows of
-// 6144 bf16: 23.8 us, 6.4 TB/s.
+// 6144 bf16: 23.8 us, 6.4 TB/s; fp32 39.6 us, 6.4 TB/s.  Other widths load single elements
+// and store single bytes, in every block: 6160 bf16 take 105 us.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kQuantWarps * 32)
     k_fp8_quantize(const void *x, size_t ld, uint32_t T, uint32_t d, uint32_t nb,
@@ -101,7 +102,9 @@ constexpr int kCombBatch = 8;  // rows of o on the way together
 // an SM) are issued before the first is used.  With enough tokens to fill the SMs a
 // CTA walks a whole token (4096 tokens of 8 rows of 6144 columns: 79.7 us, 82.5 with
 // its columns on three CTAs); with fewer a token's columns are spread over `parts`
-// CTAs (one token: 2.6 us, 4.1 on one CTA).
+// CTAs (one token: 2.6 us, 4.1 on one CTA).  Eight fp32 rows are all 64 registers of a
+// thread: 276 bytes spill, and the same 4096 tokens in fp32 take 235 us, for bytes that a
+// copy moves in 148.
 template <int DT, int YT, bool VEC>
 __global__ void __launch_bounds__(kCombThreads, 4)
     k_fp8_combine(const void *o, size_t ldo, uint32_t R, const float *w, const int32_t *pos,

@@ -13,13 +13,14 @@
 // threads' registers.
 //
 // What bounds it: the operands' way into the SM.  16384 rows of gate/up (d 6144, f 2048,
-// 16 experts) take 339 us, 2.43 PFLOP/s, and 310 with an epilogue that only releases the
-// accumulators; 4000 x 4096 x 6144 dense 81 us, 2.48 PFLOP/s, and 77.  48 KB a block in
-// ~900 clocks is 52 of the 64 bytes a clock that L2 gives an SM.  (Under a steady stream
-// of calls the card's power cap adds 5-10 %.)  The chain MMA -> loads -> FMAs -> release ->
-// MMA with two accumulators to hide it in comes next, so the latency of single
-// instructions counts: the buffers are addressed as shared memory and the roles branch on
-// a uniform warp number (through generic addresses 430 us and 115, on tid / 32 377 and 107).
+// 16 experts) take 339 us after a pause, 2.43 PFLOP/s, and 310 with an epilogue that only
+// releases the accumulators; 4000 x 4096 x 6144 dense 82 us, 2.45 PFLOP/s, and 77.  48 KB a
+// block in 900 to 950 clocks is 52 to 55 of the 64 bytes a clock that L2 gives an SM.  (In
+// a steady stream of calls the card's power cap makes them 375-392 us, 2.1-2.2 PFLOP/s,
+// and 86-89, 2.3.)  The chain MMA -> loads -> FMAs -> release -> MMA with two
+// accumulators to hide it in comes next, so the latency of single instructions counts:
+// the buffers are addressed as shared memory and the roles branch on a uniform warp
+// number (through generic addresses 430 us and 115, on tid / 32 377 and 107).
 // Measured and not kept: pairs of CTAs on 256 rows (cta_group::2, which halves an SM's
 // weight bytes: 504 and 122 against 476 and 119 us -- the other CTA's arrivals lengthen
 // the chain); accumulators of one weight block each, four in flight (494 and 131:
@@ -59,7 +60,12 @@ constexpr int kTcThreads = 12 * 32;
 constexpr uint32_t kTcStages = 4;  // of the operand ring, at most
 constexpr int kEpiWarp0 = 4;
 constexpr int kM = 128;  // rows of a tile
-constexpr int kSplitBlocks = 40;  // blocks of K from which a tile of the last round is split
+// Blocks of K from which the tiles of the last round are split.  Dense, split and whole (us):
+//   blocks             32           36           40           48
+//   16 tiles       15.7  15.8   16.4  17.1   16.9  18.5   18.3  21.2
+//   76             20.0  17.2   21.0  19.1   21.3  21.0   22.8  24.4
+//   152 and 16     32.0  31.4   34.3  34.2   35.4  37.2   39.9  43.0
+constexpr int kSplitBlocks = 40;
 // Scales of the blocks of K in flight.  A block's are written when the MMA a ring of
 // stages earlier is done, which was issued when the epilogue had read the block two
 // before that: the slot of the block two further back is free.

@@ -10,9 +10,10 @@
 // wait of the chain showed.  An accumulator takes NB MT of the 512 TMEM columns, and
 // 256 / MT of them are in flight.
 //
-// What it reaches (us, GB/s of weights; a copy reaches 6790): one token of 8 experts, d
-// 6144, f 2048: gate/up 34.3, 5870, down 21.2, 4750; 512 tokens of 256 experts,
-// gate/up 940, 6870.  A call's launch and prologue are ~5 us of each.
+// What it reaches (us, TB/s of weights; a copy reaches 6.79; the GPUs measured differ by 3
+// %): one token of 8 experts, d 6144, f 2048: gate/up 34.2-35.5, 5.7-5.9, down 21.5-22.2,
+// 4.5-4.7; 512 tokens of 256 experts, gate/up 918-950, 6.8-7.0.  A call's launch and
+// prologue are ~5 us of each.
 //
 // Epilogue warp (q, c) owns features 32q.. of both blocks for rows [c MT/2,
 // (c+1) MT/2): per block of K it adds MT/2 columns of each, times scale_w (one
@@ -456,7 +457,9 @@ cudaError_t run_few(Fp8Args &a, cudaStream_t stream) {
   // 64 SMs already draw 5.4 TB/s, and under a saturated HBM each of the split's round
   // trips (shares out, count, shares in) takes ~3 us.  Tiles of 128 columns, split and
   // whole: K 6144, 4 tiles 7.4 and 13.5 us, 32 tiles 10.6 and 13.8, 64 tiles 16.9 and 14.7;
-  // K 2048, 4 tiles 5.9 and 6.3; K 1024, 4 tiles 5.6 and 4.8.
+  // K 2048, 4 tiles 5.9 and 6.3; K 1024, 4 tiles 5.6 and 4.8.  Between 32 and 64, through
+  // the binding: 40 tiles of K 6144 12.3 and 15.0, of K 2048 9.2 and 7.6, and 40 tiles of 256
+  // columns after a round of whole ones (one token's down product, K 2048) 26.6 and 22.0.
   return launch_k(kern, sms, kFewThreads, smem, stream, true, a, maps, (uint32_t)ns,
                   a.nbk >= 16 ? sms / 4 : 0);
 }
