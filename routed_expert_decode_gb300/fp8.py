@@ -19,7 +19,7 @@ from typing import Optional
 import torch
 
 from . import moe
-from .moe import MoeError, _check, check_device_error  # noqa: F401
+from .moe import MoeError, _capturing, _check, _raw_stream, check_device_error  # noqa: F401
 
 BLOCK = 128
 SCORE_SIGMOID = moe.SCORE_SIGMOID
@@ -82,12 +82,6 @@ def lib():
 def blocks(n: int) -> int:
     """Blocks of 128 that n columns take."""
     return -(-n // BLOCK)
-
-
-# the raw handle of a device's current stream, without a torch.cuda.Stream object
-# around it (2.9 us of a call's ~6 otherwise)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -354,11 +348,14 @@ class Layer:
         self._bytes = {}    # of each set that may be dropped
         self._used_on = {}  # handles of the streams that may use each set
         self._uncleared = set()
+        self._ready = None  # the last call's set and stream: as they are for another
 
     def buffers(self, T: int, dtype: torch.dtype) -> dict:
         """The buffers of calls of T tokens of a type, made on the current stream if new."""
         key = (T, dtype)
         here = _raw_stream(self.gate.dev)
+        if self._ready == (key, here) and not _capturing():
+            return self._buffers[key]
         new = key not in self._buffers
         if new:
             E, k, d, f, R = self.E, self.router.top_k, self.d, self.f, T * self.router.top_k
@@ -388,8 +385,9 @@ class Layer:
                                self.gate.q.device)
         self._buffers[key] = b
         moe._cleared(b["ws"], key, self._uncleared, new)
-        if torch.cuda.is_current_stream_capturing():
+        if _capturing():
             self._bytes.pop(key, None)
+        self._ready = None if key in self._uncleared else (key, here)
         if new:
             self._drop_unused(key)
         return b

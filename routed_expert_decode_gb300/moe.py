@@ -193,6 +193,14 @@ def _on_stream(stream, device):
     return torch.cuda.stream(stream)
 
 
+# the raw handle of a device's current stream, without a torch.cuda.Stream object
+# around it (2.9 us), and whether the current stream is being captured
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or \
+    torch.cuda.is_current_stream_capturing
+
+
 def _used_here(used_on: set, tensors, device) -> None:
     """The current stream uses these tensors: memory belongs to the stream it was made on, and
     has to outlast the work of every other.  ``used_on``: handles of the streams known so far."""
@@ -207,7 +215,7 @@ def _cleared(ws: torch.Tensor, key, uncleared: set, new: bool) -> torch.Tensor:
     """A kept workspace, ready for a call.  One that was made while a graph was being captured
     is cleared by that graph's replays alone: until a call outside of captures has cleared it,
     each call does."""
-    capturing = torch.cuda.is_current_stream_capturing()
+    capturing = _capturing()
     if new:
         if capturing:
             uncleared.add(key)
@@ -541,6 +549,7 @@ class Layer:
         self._ws = {}
         self._used_on = {}  # handles of the streams that may use each workspace
         self._uncleared = set()
+        self._ready = None  # the last call's workspace and stream: as they are for another
 
     @classmethod
     def from_host(cls, spec, experts: dict, shared: Optional[dict], device):
@@ -568,14 +577,19 @@ class Layer:
     def workspace(self, T: int, flags=0) -> torch.Tensor:
         """The workspace of calls of T tokens, made on the current stream if new."""
         key = (T, flags & FLAG_DEBUG_TAPS)
+        here = _raw_stream(self.tensors["gate_q"].get_device())
+        if self._ready == (key, here) and not _capturing():
+            return self._ws[key]
         new = key not in self._ws
         if new:
             n = workspace_size(self.desc(flags), T)
             self._ws[key] = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.device)
-            self._used_on[key] = {torch.cuda.current_stream(self.device).cuda_stream}
+            self._used_on[key] = {here}
         else:
             _used_here(self._used_on[key], (self._ws[key],), self.device)
-        return _cleared(self._ws[key], key, self._uncleared, new)
+        _cleared(self._ws[key], key, self._uncleared, new)
+        self._ready = None if key in self._uncleared else (key, here)
+        return self._ws[key]
 
     def views(self, ws: torch.Tensor, T: int, flags=0) -> dict:
         """Typed views of the workspace regions (for taps and tests)."""
