@@ -115,7 +115,7 @@ def _rows2d(t: torch.Tensor, cols: int, name: str, dev: int):
             raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
         if dt is None:
             raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-        if step != 1 and cols > 1:
+        if step != 1 and cols > 1 and rows:
             raise ValueError(f"{name} must have consecutive columns")
         if ld < cols:
             if rows > 1:
@@ -350,6 +350,27 @@ class Layer:
         self._uncleared = set()
         self._ready = None  # the last call's set and stream: as they are for another
 
+    def _make(self, T: int, dtype: torch.dtype) -> dict:
+        """A new set of buffers, its workspace among them."""
+        E, k, d, f, R = self.E, self.router.top_k, self.d, self.f, T * self.router.top_k
+        make = self._empty
+        b = dict(idx=make((T, k), torch.int32), w=make((T, k), torch.float32),
+                 off=make((E + 1,), torch.int32), perm=make((R,), torch.int32),
+                 pos=make((T, k), torch.int32), xq=make((T, d), torch.float8_e4m3fn),
+                 xs=make((T, blocks(d)), torch.float32),
+                 hq=make((R, f), torch.float8_e4m3fn),
+                 hs=make((R, blocks(f)), torch.float32), o=make((R, d), dtype), shared=None)
+        if self.shared is not None:
+            fs = self.shared[0].N
+            b.update(shq=make((T, fs), torch.float8_e4m3fn),
+                     shs=make((T, blocks(fs)), torch.float32), shared=make((T, d), dtype))
+        n = max(group_route_workspace_size(self.router, T), workspace_size(max(R, T)))
+        b["ws"] = torch.zeros(n, dtype=torch.uint8, device=self.gate.q.device)
+        return b
+
+    def _empty(self, shape, dtype) -> torch.Tensor:
+        return torch.empty(shape, dtype=dtype, device=self.gate.q.device)
+
     def buffers(self, T: int, dtype: torch.dtype) -> dict:
         """The buffers of calls of T tokens of a type, made on the current stream if new."""
         key = (T, dtype)
@@ -358,23 +379,7 @@ class Layer:
             return self._buffers[key]
         new = key not in self._buffers
         if new:
-            E, k, d, f, R = self.E, self.router.top_k, self.d, self.f, T * self.router.top_k
-
-            def make(shape, dt):
-                return torch.empty(shape, dtype=dt, device=self.gate.q.device)
-
-            b = dict(idx=make((T, k), torch.int32), w=make((T, k), torch.float32),
-                     off=make((E + 1,), torch.int32), perm=make((R,), torch.int32),
-                     pos=make((T, k), torch.int32), xq=make((T, d), torch.float8_e4m3fn),
-                     xs=make((T, blocks(d)), torch.float32),
-                     hq=make((R, f), torch.float8_e4m3fn),
-                     hs=make((R, blocks(f)), torch.float32), o=make((R, d), dtype), shared=None)
-            if self.shared is not None:
-                fs = self.shared[0].N
-                b.update(shq=make((T, fs), torch.float8_e4m3fn),
-                         shs=make((T, blocks(fs)), torch.float32), shared=make((T, d), dtype))
-            n = max(group_route_workspace_size(self.router, T), workspace_size(max(R, T)))
-            b["ws"] = torch.zeros(n, dtype=torch.uint8, device=self.gate.q.device)
+            b = self._make(T, dtype)
             self._bytes[key] = sum(t.numel() * t.element_size() for t in b.values()
                                    if t is not None)
             self._used_on[key] = {here}
@@ -419,20 +424,32 @@ class Layer:
             with torch.cuda.device(self.gate.dev):
                 return self.forward(x, logits, bias, y)
         T = x.shape[0]
-        k = self.router.top_k
         b = self.buffers(T, x.dtype)
         if y is None:
             y = torch.empty((T, self.d), dtype=x.dtype, device=x.device)
+        group_route(self.router, logits, bias, b["idx"], b["w"], b["off"], b["perm"], b["pos"],
+                    b["ws"])
+        self._experts(b, x)
+        combine(b["o"], b["w"], b["pos"], y, shared=b["shared"])
+        return LayerOutput(y=y, **{n: b[n] for n in ("idx", "w", "off", "perm", "pos", "xq", "xs",
+                                                     "hq", "hs", "o", "shared")})
+
+    def _experts(self, b: dict, x: torch.Tensor) -> None:
+        """The experts' rows b["o"] and the shared expert's b["shared"] of x, once it is routed."""
         ws = b["ws"]
-        group_route(self.router, logits, bias, b["idx"], b["w"], b["off"], b["perm"], b["pos"], ws)
         quantize(x, b["xq"], b["xs"])
         swiglu(self.gate, self.up, b["xq"], b["xs"], b["hq"], b["hs"], ws, off=b["off"],
-               perm=b["perm"], top_k=k)
+               perm=b["perm"], top_k=self.router.top_k)
         product(self.down, b["hq"], b["hs"], b["o"], ws, off=b["off"])
         if self.shared is not None:
             sg, su, sd = self.shared
             swiglu(sg, su, b["xq"], b["xs"], b["shq"], b["shs"], ws)
             product(sd, b["shq"], b["shs"], b["shared"], ws)
-        combine(b["o"], b["w"], b["pos"], y, shared=b["shared"])
-        return LayerOutput(y=y, **{n: b[n] for n in ("idx", "w", "off", "perm", "pos", "xq", "xs",
-                                                     "hq", "hs", "o", "shared")})
+
+    def router_gradients(self, out: LayerOutput, logits: torch.Tensor, dy: torch.Tensor, **kw):
+        """What ``dy``, the gradient of ``out.y``, says of the router: see
+        ``router_grad.layer_gradients``.  ``out`` is of this layer's last call with as many
+        tokens and the same logits."""
+        from . import router_grad
+
+        return router_grad.layer_gradients(self.router, out, logits, dy, **kw)
