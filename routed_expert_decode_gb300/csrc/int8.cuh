@@ -24,5 +24,9 @@ struct Int8Call {
 };
 size_t int8_gemm_ws(uint32_t rows);
 cudaError_t launch_int8_gemm(const Int8Call &c);
+// the tensor-core products (int8_tc.cu): operands that tensor copies can take
+bool int8_tc_ok(const Fp8Args &a);
+size_t int8_tc_ws(uint32_t rows);
+cudaError_t launch_int8_tc(Fp8Args &a, bool swiglu, cudaStream_t stream);
 
 }  // namespace moe

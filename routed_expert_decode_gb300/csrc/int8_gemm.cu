@@ -106,8 +106,7 @@ cudaError_t run_core(Fp8Args &a, cudaStream_t stream) {
 }  // namespace
 
 size_t int8_gemm_ws(uint32_t rows) {
-  (void)rows;
-  return MOE_WS_FIXED_BYTES;
+  return MOE_WS_FIXED_BYTES + int8_tc_ws(rows);
 }
 
 cudaError_t launch_int8_gemm(const Int8Call &c) {
@@ -134,6 +133,7 @@ cudaError_t launch_int8_gemm(const Int8Call &c) {
   a.err = (uint32_t *)c.ws;
   a.sync = (uint32_t *)(c.ws + 256) + kFp8TileSync;
   a.part = (float *)(c.ws + MOE_WS_FIXED_BYTES);
+  if (int8_tc_ok(a)) return launch_int8_tc(a, c.swiglu, c.stream);
   return c.swiglu ? run_core<true>(a, c.stream) : run_core<false>(a, c.stream);
 }
 
