@@ -12,17 +12,30 @@
 // come as bytes by TMA, and the converting warps write them to TMEM, from where the MMA
 // takes its A operand, so that they cross shared memory once, as bytes.  The activation
 // rows are the N side: the converting warps fetch their bytes through perm straight to
-// registers, two steps of K ahead, and store fp16 in the swizzled layout.  The MMA's N is
-// the tile's rows rounded up to 16.
+// registers, a block of 128 codes ahead, and store fp16 in the swizzled layout.  The MMA's
+// N is the tile's rows rounded up to 16.
+//
+// Experts with many rows: two CTAs work on a tile of 256 weight rows (cta_group::2), each
+// with its own 128 in its TMEM and half of the activation rows in its shared memory.  One
+// CTA's N side alone, fp16 written and read again, is all that its shared memory can move
+// while the tensor cores work (128 bytes a clock), and the fetches come on top: 16384 rows
+// of gate/up (d 6144, f 2048, 16 experts) take 770 us so, 532 in pairs (1.55 PFLOP/s; 470
+// without the conversions).  The first CTA issues; what it has to know of the second
+// one's warps goes over four relaying warps there, because an arrival that makes the work
+// behind it visible to the other CTA takes ~800 clocks: with one warp for it 976 us, with the
+// converting warps making theirs 1390.
 //
 // TMEM lane 32q + i is a weight row; for SwiGLU lanes i < 16 of a quarter hold gate rows
 // and the others the up rows of the same 16 features, so that g and u meet by one
 // shuffle for two activation rows.
 //
-// Warps: 0 weights by TMA, 1 TMEM owner and MMA issuer, 2..9 weight converters (one set
-// of four for each half of a stage's 128 codes), then the epilogue's, then the activation
-// converters.  The work goes out over one CTA per SM as Walk says; the shares of a
-// split tile meet in the workspace, where the last to arrive adds all of them in order.
+// Loads of the activations take whole lines, eight lanes a row, and may stay in L1: 64
+// bytes a row and step, past L1, cost 1080 us in place of 790 (with one CTA a tile).
+//
+// Warps: 0 weights by TMA, 1 TMEM owner and MMA issuer, then the weight converters (sets of
+// four), the epilogue's, the activation converters and the relays.  The work goes out
+// over one CTA (or pair) per SM as Walk says; the shares of a split tile meet in the
+// workspace, where the last to arrive adds all of them in order.
 #include <string.h>
 
 #include "fp8_tc_ptx.cuh"
@@ -31,22 +44,37 @@
 namespace moe {
 namespace {
 
-constexpr uint32_t kAColumn = 256;  // first TMEM column of the weights' ring
-
-template <bool SWIGLU, int NT>
+// NT: rows of a tile.  PAIR: a tile of twice the weight rows by two CTAs (cta_group::2), each
+// with its own weight rows in its TMEM and half of the activation rows in its shared memory.
+template <int NT, bool PAIR>
 struct Shape {
-  static constexpr uint32_t accs = 256 / NT;               // accumulators, NT columns each
-  static constexpr uint32_t ring = NT == 256 ? 4 : 8;      // stages of 64 along K
-  static constexpr uint32_t x_bytes = NT * 128;            // activations of a stage
-  static constexpr int epi = NT >= 128 ? 8 : 4;            // epilogue warps
-  static constexpr int sets = NT == 256 ? 1 : 2;           // sets of activation converters
-  static constexpr int x_warps = NT / 32;                  // warps of a set
-  static constexpr int epi0 = 10, x0 = epi0 + epi;         // first warps
-  static constexpr int threads = (x0 + sets * x_warps) * 32;
-  static constexpr int cols = NT / (epi / 4);              // columns of an epilogue warp
-  static constexpr bool split = NT <= 64;                  // tiles may be shared along K
+  static constexpr uint32_t accs = 256 / NT;                 // accumulators, NT columns each
+  static constexpr uint32_t a_column = 256;                  // first TMEM column of the weights
+  static constexpr uint32_t ring = 8;                        // stages of 64 along K
+  static constexpr int rows = PAIR ? NT / 2 : NT;            // activation rows of a CTA
+  static constexpr uint32_t x_bytes = rows * 128;            // ... and their bytes in a stage
+  static constexpr int epi = NT >= 128 ? 8 : 4;              // epilogue warps
+  static constexpr int w_sets = NT >= 128 ? 1 : 2;           // sets of weight converters
+  static constexpr int x_warps = rows / 32;                  // activation converters of a set
+  static constexpr int sets = NT >= 128 ? 2 : 4;                 // sets of them
+  static constexpr int epi0 = 2 + 4 * w_sets, x0 = epi0 + epi;  // first warps
+  static constexpr int relay0 = x0 + sets * x_warps;          // a pair's relaying warps
+  static constexpr int relays = PAIR ? 4 : 0;
+  static constexpr int threads = (relay0 + relays) * 32;
+  static constexpr int cols = NT / (epi / 4);                // columns of an epilogue warp
+  static constexpr bool split = !PAIR && NT <= 64;           // tiles may be shared along K
+  static constexpr int ctas = PAIR ? 2 : 1;
+  static_assert(sets <= (int)ring / 2 && cols % 32 == 0, "");
 };
 
+// 16 bytes that other loads of this SM may want again.  Volatile, as ld_once16.
+__device__ __forceinline__ uint4 ld_again16(const void *p) {
+  uint4 w;
+  asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+               : "l"(p));
+  return w;
+}
 // four codes to fp16
 __device__ __forceinline__ void i8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
   const uint32_t u = w ^ 0x80808080u;
@@ -74,19 +102,84 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32])
 
 // D (+)= A B^T over 64 codes of K: four MMAs of K = 16, 8 TMEM columns of A and 32 bytes of
 // B's rows apart.  Called by a whole converged warp with uniform operands; one lane issues.
+template <bool PAIR>
 __device__ __forceinline__ void tc_mma_step(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                             bool add) {
+  if (PAIR)
+    asm volatile(
+        "{\n .reg .pred e, f, t;\n .reg .b64 b1, b2, b3;\n .reg .b32 a1, a2, a3;\n"
+        " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+        " add.u32 a1, %1, 8;\n add.u32 a2, %1, 16;\n add.u32 a3, %1, 24;\n"
+        " setp.ne.b32 f, %4, 0;\n setp.eq.b32 t, 0, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, f;\n"
+        " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [a1], b1, %3, t;\n"
+        " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [a2], b2, %3, t;\n"
+        " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [a3], b3, %3, t;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred e, f, t;\n .reg .b64 b1, b2, b3;\n .reg .b32 a1, a2, a3;\n"
+        " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+        " add.u32 a1, %1, 8;\n add.u32 a2, %1, 16;\n add.u32 a3, %1, 24;\n"
+        " setp.ne.b32 f, %4, 0;\n setp.eq.b32 t, 0, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// arrive on the barrier (PAIR: of the CTAs in the mask) when the MMAs so far are done
+template <bool PAIR>
+__device__ __forceinline__ void tc_commit_all(uint64_t *bar, uint16_t ctas = 3) {
+  if (!PAIR) return tc_commit(bar);
   asm volatile(
-      "{\n .reg .pred e, f, t;\n .reg .b64 b1, b2, b3;\n .reg .b32 a1, a2, a3;\n"
-      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
-      " add.u32 a1, %1, 8;\n add.u32 a2, %1, 16;\n add.u32 a3, %1, 24;\n"
-      " setp.ne.b32 f, %4, 0;\n setp.eq.b32 t, 0, 0;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;\n}\n" ::"r"(s32(bar)),
+      "h"(ctas)
       : "memory");
+}
+// the first CTA's barrier at this place, as an address of the pair
+__device__ __forceinline__ uint32_t leader_bar(uint64_t *b) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(s32(b)));
+  return r;
+}
+// one arrival on the barrier that the MMA's issuer waits on
+template <bool PAIR>
+__device__ __forceinline__ void arrive_issuer(uint64_t *b) {
+  if (!PAIR) return bar_arrive(b);
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_bar(b))
+               : "memory");
+}
+// bar_wait for arrivals of both CTAs
+__device__ __forceinline__ bool pair_try(uint64_t *b, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(s32(b)), "r"(parity), "n"(kHintNs)
+      : "memory");
+  return done != 0;
+}
+template <bool PAIR>
+__device__ __forceinline__ void issuer_wait(uint64_t *b, uint32_t parity, const Guard &g) {
+  if (!PAIR) return bar_wait(b, parity, g);
+  if (pair_try(b, parity) || *g.abort_flag) return;
+  const long long t0 = clock64();
+  for (int i = 0; i < kSpin && !*g.abort_flag; ++i) {
+    if (pair_try(b, parity)) return;
+    if (clock64() - t0 > kWaitCycles) break;
+  }
+  if (!*g.abort_flag) atomicOr(g.err, kErrTimeout);
+  *g.abort_flag = 1;
+}
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // a place in a ring that is passed `step` stages at a time
@@ -103,12 +196,12 @@ struct StepRing {
   }
 };
 
-template <bool SWIGLU, int NT>
-__global__ void __launch_bounds__(Shape<SWIGLU, NT>::threads, 1)
+template <bool SWIGLU, int NT, bool PAIR>
+__global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
     k_int8_tc(const Fp8Args a, const __grid_constant__ Fp8Maps maps, const uint32_t n_w,
               const int split_below) {
   pdl_trigger();
-  using S = Shape<SWIGLU, NT>;
+  using S = Shape<NT, PAIR>;
   extern __shared__ __align__(1024) uint8_t tsm_raw[];
   uint8_t *tsm = tsm_raw + ((0u - s32(tsm_raw)) & 1023u);  // stays a shared address
   const int tid = threadIdx.x, lane = tid & 31;
@@ -137,13 +230,13 @@ __global__ void __launch_bounds__(Shape<SWIGLU, NT>::threads, 1)
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       bar_init(&w_full[i], 1);
-      bar_init(&w_empty[i], 8);
+      bar_init(&w_empty[i], 4 * S::w_sets);
     }
     for (uint32_t i = 0; i < 8; ++i) {
-      bar_init(&full[i], 4 + S::x_warps);
+      bar_init(&full[i], 4 + S::x_warps + (PAIR && !(blockIdx.x & 1)));
       bar_init(&empty[i], 1);
       bar_init(&d_full[i], 1);
-      bar_init(&d_empty[i], S::epi);
+      bar_init(&d_empty[i], S::ctas * S::epi);
     }
     bar_init(meet_bar, S::epi);
     bar_init(drain, 1);
@@ -151,21 +244,35 @@ __global__ void __launch_bounds__(Shape<SWIGLU, NT>::threads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                     s32(tmem_holder))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                       s32(tmem_holder))
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                       s32(tmem_holder))
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) pair_sync();  // the other CTA's barriers are there
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   fp8_warm(a);
   pdl_wait();
   const RowTiles rt = fp8_row_tiles<NT>(a, tiles_sm);
-  Walk walk(rt.total * (int)a.n_tiles, a, (int)blockIdx.x, (int)gridDim.x, split_below);
+  const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;
+  Walk walk(rt.total * (int)a.n_tiles, a, (int)blockIdx.x / S::ctas, (int)gridDim.x / S::ctas,
+            split_below);
   Seg seg;
   const Guard guard{a.err, abort_flag};
+  // this CTA's block of weight rows
+  auto block_of = [&](const Fp8Tile &t) { return t.nt * S::ctas + rank; };
+  // columns of the MMA: the tile's rows, rounded up so that each CTA has a multiple of 16
+  auto mma_rows = [](int rows) { return PAIR ? (rows + 31) & ~31 : (rows + 15) & ~15; };
 
   if (warp == 0) {
     // ============================ weights
@@ -180,10 +287,10 @@ __global__ void __launch_bounds__(Shape<SWIGLU, NT>::threads, 1)
         uint8_t *dst = tsm + st.i * kWBytes;
         bar_expect(&w_full[st.i], kWBytes);
         if (SWIGLU) {
-          tma_w(dst, &maps.w[0], kb * 128, t.nt * 64, t.e, &w_full[st.i]);
-          tma_w(dst + kWBytes / 2, &maps.w[1], kb * 128, t.nt * 64, t.e, &w_full[st.i]);
+          tma_w(dst, &maps.w[0], kb * 128, block_of(t) * 64, t.e, &w_full[st.i]);
+          tma_w(dst + kWBytes / 2, &maps.w[1], kb * 128, block_of(t) * 64, t.e, &w_full[st.i]);
         } else {
-          tma_w(dst, &maps.w[0], kb * 128, t.nt * 128, t.e, &w_full[st.i]);
+          tma_w(dst, &maps.w[0], kb * 128, block_of(t) * 128, t.e, &w_full[st.i]);
         }
       }
     }
@@ -192,66 +299,78 @@ __global__ void __launch_bounds__(Shape<SWIGLU, NT>::threads, 1)
       if (!bar_wait_for(*abort_flag ? &w_full[st.i] : &w_empty[st.i], st.phase ^ 1))
         atomicOr(a.err, kErrTimeout);
   } else if (warp == 1) {
-    // ============================ MMA issuer
+    // ============================ MMA issuer (of a pair, the first CTA's)
     Ring st, acc;
     while (!guard.aborted() && walk.take(seg)) {
-      const Fp8Tile t = fp8_tile<NT>(a, rt, seg.tile);
-      const uint32_t idesc = idesc_for((uint32_t)(t.rows + 15) & ~15u);
-      const uint32_t d = tmem + acc.i * NT;
-      bar_wait(&d_empty[acc.i], acc.phase ^ 1, guard);
       const int steps = 2 * (seg.kb1 - seg.kb0);
+      if (PAIR && rank) {  // follows the ring, for its end
+        for (int s = 0; s < steps; ++s) st.next(S::ring);
+        continue;
+      }
+      const Fp8Tile t = fp8_tile<NT>(a, rt, seg.tile);
+      // M = 128, or 256 of a pair
+      const uint32_t idesc = idesc_for((uint32_t)mma_rows(t.rows)) + (PAIR ? 8u << 24 : 0u);
+      const uint32_t d = tmem + acc.i * NT;
+      issuer_wait<PAIR>(&d_empty[acc.i], acc.phase ^ 1, guard);
       for (int s = 0; s < steps; ++s, st.next(S::ring)) {
-        bar_wait(&full[st.i], st.phase, guard);
+        issuer_wait<PAIR>(&full[st.i], st.phase, guard);
         tc_fence_after();
         __syncwarp();
-        tc_mma_step(d, tmem + kAColumn + st.i * 32, sw128_desc(s32(xsm + st.i * S::x_bytes)),
-                    idesc, s > 0);
-        tc_commit(&empty[st.i]);
+        tc_mma_step<PAIR>(d, tmem + S::a_column + st.i * 32,
+                          sw128_desc(s32(xsm + st.i * S::x_bytes)), idesc, s > 0);
+        tc_commit_all<PAIR>(&empty[st.i]);
       }
-      tc_commit(&d_full[acc.i]);
+      tc_commit_all<PAIR>(&d_full[acc.i]);
       acc.next(S::accs);
     }
     if (guard.aborted()) {
-      tc_commit(drain);
-      bar_wait_for(drain, 0);
+      if (!rank) {
+        tc_commit_all<PAIR>(drain, 1);
+        bar_wait_for(drain, 0);
+      }
     } else {  // the last steps' arrivals
       for (uint32_t i = 0; i < S::ring; ++i, st.next(S::ring))
         if (!bar_wait_for(&empty[st.i], st.phase ^ 1)) atomicOr(a.err, kErrTimeout);
     }
   } else if (warp < S::epi0) {
     // ============================ weight converters: half `set` of each stage
-    const int set = (warp - 2) >> 2, quarter = warp & 3;
+    const int set = S::w_sets == 2 ? (warp - 2) >> 2 : 0, quarter = warp & 3;
     const int row = SWIGLU ? quarter * 16 + (lane & 15) + (lane >> 4) * 64 : quarter * 32 + lane;
-    const uint32_t dst = tmem + kAColumn + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t dst = tmem + S::a_column + ((uint32_t)(quarter * 32) << 16);
     Ring ws;
-    StepRing<2> st(set);
+    StepRing<S::w_sets> st(set);
     while (!guard.aborted() && walk.take(seg)) {
-      for (int kb = seg.kb0; kb < seg.kb1; ++kb, ws.next(n_w), st.next(S::ring)) {
+      for (int kb = seg.kb0; kb < seg.kb1; ++kb, ws.next(n_w)) {
         bar_wait(&w_full[ws.i], ws.phase, guard);
         // 128-byte swizzle: chunk c of row r at c ^ (r % 8)
         const uint8_t *src = tsm + ws.i * kWBytes + row * 128;
-        uint4 v[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          v[c] = *(const uint4 *)(src + (((set * 4 + c) ^ (row & 7)) << 4));
-        __syncwarp();
-        if (lane == 0) bar_arrive(&w_empty[ws.i]);
-        uint32_t r[32];
+        for (int h = set; h < 2; h += S::w_sets, st.next(S::ring)) {
+          uint4 v[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          i8x4_to_f16(v[c].x, r[8 * c], r[8 * c + 1]);
-          i8x4_to_f16(v[c].y, r[8 * c + 2], r[8 * c + 3]);
-          i8x4_to_f16(v[c].z, r[8 * c + 4], r[8 * c + 5]);
-          i8x4_to_f16(v[c].w, r[8 * c + 6], r[8 * c + 7]);
+          for (int c = 0; c < 4; ++c)
+            v[c] = *(const uint4 *)(src + (((h * 4 + c) ^ (row & 7)) << 4));
+          if (S::w_sets == 2 || h == 1) {
+            __syncwarp();
+            if (lane == 0) bar_arrive(&w_empty[ws.i]);
+          }
+          uint32_t r[32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            i8x4_to_f16(v[c].x, r[8 * c], r[8 * c + 1]);
+            i8x4_to_f16(v[c].y, r[8 * c + 2], r[8 * c + 3]);
+            i8x4_to_f16(v[c].z, r[8 * c + 4], r[8 * c + 5]);
+            i8x4_to_f16(v[c].w, r[8 * c + 6], r[8 * c + 7]);
+          }
+          bar_wait(&empty[st.i], st.phase ^ 1, guard);
+          tc_fence_after();
+          __syncwarp();
+          tc_st32(dst + st.i * 32, r);
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&full[st.i]);
         }
-        bar_wait(&empty[st.i], st.phase ^ 1, guard);
-        tc_fence_after();
-        __syncwarp();
-        tc_st32(dst + st.i * 32, r);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&full[st.i]);
       }
     }
   } else if (warp < S::x0) {
@@ -271,8 +390,8 @@ __global__ void __launch_bounds__(Shape<SWIGLU, NT>::threads, 1)
       float *xs = xsc + (tiles++ & 1) * NT;
       for (int r = ew * 32 + lane; r < t.rows; r += S::epi * 32)
         xs[r] = a.xs[max(0, fp8_x_row(a, t.row0 + r))];
-      const uint32_t n = SWIGLU ? (uint32_t)t.nt * 64 + quarter * 16 + (lane & 15)
-                                : (uint32_t)t.nt * 128 + quarter * 32 + lane;
+      const uint32_t n = SWIGLU ? (uint32_t)block_of(t) * 64 + quarter * 16 + (lane & 15)
+                                : (uint32_t)block_of(t) * 128 + quarter * 32 + lane;
       const bool up = SWIGLU && lane >= 16;
       const float ws = n < a.N ? a.wsc[up ? 1 : 0][(size_t)t.e * a.N + n] : 0.0f;
       meet();
@@ -291,21 +410,28 @@ __global__ void __launch_bounds__(Shape<SWIGLU, NT>::threads, 1)
         }
         auto store = [&](auto *p, auto from) {
           p += (size_t)(t.row0 + c) * a.ld + n;
-          if (!SWIGLU) {
+          // eight rows at a time without a branch between them: their latencies overlap
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (i >= rows) break;
-              if (n < a.N) p[(size_t)i * a.ld] = from(s[i]);
-            }
-          } else {
+          for (int i0 = 0; i0 < 32; i0 += 8) {
+            if (i0 >= rows) break;  // the warp alike
+            if (!SWIGLU) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              if (i >= rows) break;  // the warp alike
-              // lanes of gate rows take row i, those of up rows row i + 1
-              const float got = __shfl_xor_sync(0xffffffffu, up ? s[i] : s[i + 1], 16);
-              const float h = up ? fp8_swiglu_value(got, s[i + 1]) : fp8_swiglu_value(s[i], got);
-              const int r = i + up;
-              if (n < a.N && r < rows) p[(size_t)r * a.ld] = from(h);
+              for (int i = i0; i < i0 + 8; ++i)
+                if (n < a.N && i < rows) p[(size_t)i * a.ld] = from(s[i]);
+            } else {
+              float h[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                // lanes of gate rows take row i0 + 2i, those of up rows the next
+                const float x = s[i0 + 2 * i], y = s[i0 + 2 * i + 1];
+                const float got = __shfl_xor_sync(0xffffffffu, up ? x : y, 16);
+                h[i] = fp8_swiglu_value(up ? got : x, up ? y : got);
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = i0 + 2 * i + up;
+                if (n < a.N && r < rows) p[(size_t)r * a.ld] = from(h[i]);
+              }
             }
           }
         };
@@ -327,11 +453,11 @@ __global__ void __launch_bounds__(Shape<SWIGLU, NT>::threads, 1)
           if (c + 32 >= S::cols || c0 + c + 32 >= t.rows) {  // the last of this warp's
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(&d_empty[dr.i]);
+            if (lane == 0) arrive_issuer<PAIR>(&d_empty[dr.i]);
           }
           emit(c0 + c, v);
         }
-        if (c0 >= t.rows && lane == 0) bar_arrive(&d_empty[dr.i]);
+        if (c0 >= t.rows && lane == 0) arrive_issuer<PAIR>(&d_empty[dr.i]);
         dr.next(S::accs);
         continue;
       }
@@ -355,7 +481,7 @@ __global__ void __launch_bounds__(Shape<SWIGLU, NT>::threads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) bar_arrive(&d_empty[dr.i]);
+      if (lane == 0) arrive_issuer<PAIR>(&d_empty[dr.i]);
       dr.next(S::accs);
       __threadfence();
       meet();
@@ -384,91 +510,111 @@ __global__ void __launch_bounds__(Shape<SWIGLU, NT>::threads, 1)
         emit(c, v);
       }
     }
+  } else if (PAIR && warp >= S::relay0) {
+    // ============================ relay: passes the second CTA's arrivals on to the issuer.
+    // Such an arrival makes all that it follows visible to the other CTA, ~800 clocks
+    // each: several are on the way together.
+    StepRing<PAIR ? S::relays : 1> st(warp - S::relay0);
+    int first = warp - S::relay0;
+    while (rank && !guard.aborted() && walk.take(seg)) {
+      const int steps = 2 * (seg.kb1 - seg.kb0);
+      for (int s = first; s < steps; s += PAIR ? S::relays : 1, st.next(S::ring)) {
+        bar_wait(&full[st.i], st.phase, guard);
+        __syncwarp();
+        if (lane == 0) arrive_issuer<true>(&full[st.i]);
+      }
+      first = (first - steps % (PAIR ? S::relays : 1) + S::relays) % (PAIR ? S::relays : 1);
+    }
   } else {
-    // ============================ activation converters: four lanes a row of 64 codes
+    // ============================ activation converters: eight lanes a row of 128 codes, the
+    // first four of which write a block's first step and the others its second
     const int xw = warp - S::x0, set = xw / S::x_warps;
-    const int th = (xw - set * S::x_warps) * 32 + lane, chunk = th & 3, r0 = th >> 2;
-    constexpr int kPass = NT / 4;  // rows of a pass over the set's threads
+    const int th = (xw - set * S::x_warps) * 32 + lane, chunk = th & 7, r0 = th >> 3;
+    const int step = chunk >> 2, c0 = 2 * (chunk & 3);  // 16-byte chunks c0, c0 + 1 of fp16
+    constexpr int kPass = S::x_warps * 4, kPasses = 8;  // rows of a pass over the set's threads
+    constexpr uint32_t kBlocks = S::ring / 2;
     StepRing<S::sets> st(set);
+    int first = set;  // this set's first block of the segment
     while (!guard.aborted() && walk.take(seg)) {
       const Fp8Tile t = fp8_tile<NT>(a, rt, seg.tile);
-      const int rows16 = (t.rows + 15) & ~15;
-      int row[4];  // a bad one (flagged) reads row 0
+      const int rows = mma_rows(t.rows) / S::ctas;  // this CTA's
+      int row[kPasses];  // a bad one (flagged) reads row 0
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        row[j] = r0 + j * kPass < t.rows ? max(0, fp8_x_row(a, t.row0 + r0 + j * kPass)) : -1;
-      const uint32_t k0 = (uint32_t)seg.kb0 * 128 + chunk * 16;
-      const int steps = 2 * (seg.kb1 - seg.kb0);
-      auto load = [&](uint4 (&v)[4], int s) {
-        const uint32_t k = k0 + s * 64;
+      for (int j = 0; j < kPasses; ++j) {
+        const int r = rank * rows + r0 + j * kPass;
+        row[j] = r0 + j * kPass < rows && r < t.rows ? max(0, fp8_x_row(a, t.row0 + r)) : -1;
+      }
+      uint4 v[kPasses];
+      auto load = [&](int kb) {
+        const uint32_t k = (uint32_t)kb * 128 + chunk * 16;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kPasses; ++j) {
           v[j] = make_uint4(0, 0, 0, 0);
-          if (s < steps && row[j] >= 0 && k < a.K)
-            v[j] = ld_once16(a.xq + (size_t)(uint32_t)row[j] * a.K + k);
+          if (kb < seg.kb1 && row[j] >= 0 && k < a.K)
+            v[j] = ld_again16(a.xq + (size_t)(uint32_t)row[j] * a.K + k);
         }
       };
-      auto convert = [&](const uint4 (&v)[4]) {
-        bar_wait(&empty[st.i], st.phase ^ 1, guard);
-        const uint32_t buf = s32(xsm + st.i * S::x_bytes);
+      load(seg.kb0 + first);
+      for (int kb = seg.kb0 + first; kb < seg.kb1; kb += S::sets) {
+        bar_wait(&empty[2 * st.i], st.phase ^ 1, guard);
+        bar_wait(&empty[2 * st.i + 1], st.phase ^ 1, guard);
+        const uint32_t buf = s32(xsm + (2 * st.i + step) * S::x_bytes);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kPasses; ++j) {
           const int r = r0 + j * kPass;
-          if (r >= rows16) break;
+          if (r >= rows) break;
           uint32_t h[8];
           i8x4_to_f16(v[j].x, h[0], h[1]);
           i8x4_to_f16(v[j].y, h[2], h[3]);
           i8x4_to_f16(v[j].z, h[4], h[5]);
           i8x4_to_f16(v[j].w, h[6], h[7]);
-          // 128-byte swizzle: chunk c of row r at c ^ (r % 8)
+          // 128-byte swizzle: chunk c of row r at c ^ (r % 8).  The second step's lanes
+          // store their second chunk first, so that eight lanes meet all banks.
           const uint32_t at = buf + r * 128;
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
-                           at + (((2 * chunk) ^ (r & 7)) << 4)),
-                       "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
-                       : "memory");
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
-                           at + (((2 * chunk + 1) ^ (r & 7)) << 4)),
-                       "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
-                       : "memory");
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const bool second = q != step;
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                             at + (((c0 + second) ^ (r & 7)) << 4)),
+                         "r"(second ? h[4] : h[0]), "r"(second ? h[5] : h[1]),
+                         "r"(second ? h[6] : h[2]), "r"(second ? h[7] : h[3])
+                         : "memory");
+          }
         }
         fence_async();  // read by the tensor core's proxy
         __syncwarp();
-        if (lane == 0) bar_arrive(&full[st.i]);
-        st.next(S::ring);
-      };
-      uint4 v0[4], v1[4];
-      load(v0, set);
-      load(v1, set + S::sets);
-      for (int s = set; s < steps; s += 2 * S::sets) {
-        convert(v0);
-        load(v0, s + 2 * S::sets);
-        if (s + S::sets < steps) {
-          convert(v1);
-          load(v1, s + 3 * S::sets);
-        }
+        if (lane < 2) bar_arrive(&full[2 * st.i + lane]);
+        st.next(kBlocks);
+        load(kb + S::sets);
       }
+      first = (first - (seg.kb1 - seg.kb0) % S::sets + S::sets) % S::sets;
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) pair_sync();  // neither CTA leaves while the other may reach its memory
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
 
-template <bool SWIGLU, int NT>
+template <bool SWIGLU, int NT, bool PAIR>
 cudaError_t run_tc(Fp8Args &a, cudaStream_t stream) {
-  using S = Shape<SWIGLU, NT>;
-  const int sms = fp8_ctas();
-  const uint32_t channels = SWIGLU ? 64 : 128;
-  fp8_set_tiles(a, (a.N + channels - 1) / channels, sms);
+  using S = Shape<NT, PAIR>;
+  const int sms = fp8_ctas() / S::ctas * S::ctas;
+  if (sms < S::ctas) return cudaErrorInvalidValue;
+  const uint32_t channels = SWIGLU ? 64 : 128;  // of a CTA
+  fp8_set_tiles(a, (a.N + channels * S::ctas - 1) / (channels * S::ctas), sms / S::ctas);
   a.part_stride = (size_t)NT * 128;
   Fp8Maps maps;
   memset(&maps, 0, sizeof maps);
   for (int m = 0; m < (SWIGLU ? 2 : 1); ++m)
     if (!byte_map(&maps.w[m], a.wq[m], a.K, a.N, a.E, 3, channels)) return cudaErrorInvalidValue;
-  auto kern = k_int8_tc<SWIGLU, NT>;
+  auto kern = k_int8_tc<SWIGLU, NT, PAIR>;
   const size_t rest =
       1024 + S::ring * (size_t)S::x_bytes + 512 + 4 * 2 * NT + fp8_tiles_smem(a.E);
   int n_w = (int)((kSmemLimit - rest) / kWBytes);
@@ -477,17 +623,29 @@ cudaError_t run_tc(Fp8Args &a, cudaStream_t stream) {
   static std::atomic<bool> done[kMaxDevices];
   const cudaError_t e = allow_smem(kern, done);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, sms, S::threads, smem, stream, true, a, maps, (uint32_t)n_w,
-                  S::split && a.nbk >= 16 ? sms / 4 : 0);
+  const int split_below = S::split && a.nbk >= 16 ? sms / 4 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = sms;
+  cfg.blockDim = S::threads;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {2, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, maps, (uint32_t)n_w, split_below);
 }
 
 template <bool SWIGLU>
 cudaError_t run_by_rows(Fp8Args &a, cudaStream_t stream) {
   const uint64_t R = a.R, E = a.E;
-  if (R <= 24 * E) return run_tc<SWIGLU, 32>(a, stream);
-  if (R <= 64 * E) return run_tc<SWIGLU, 64>(a, stream);
-  if (R <= 128 * E) return run_tc<SWIGLU, 128>(a, stream);
-  return run_tc<SWIGLU, 256>(a, stream);
+  if (R <= 24 * E) return run_tc<SWIGLU, 32, false>(a, stream);
+  if (R <= 64 * E) return run_tc<SWIGLU, 64, false>(a, stream);
+  if (R <= 128 * E) return run_tc<SWIGLU, 128, false>(a, stream);
+  return run_tc<SWIGLU, 256, true>(a, stream);
 }
 
 }  // namespace
