@@ -10,20 +10,39 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kBackCtas = 4;  // CTAs an SM of the logits' gradient (65536 x 256 bf16: 39 us, 43 with 3)
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kAll = 0xffffffffu;
 
+// WIDE: teams of 32 lanes, known when compiling; else of a power of two below
+template <bool WIDE>
 struct Team {
-  uint32_t lanes;  // a power of two; NC > 1 chunks only with 32
-  int l, t;        // lane within the team, team within the warp
-  __device__ __forceinline__ uint32_t per_warp() const { return 32 / lanes; }
-  __device__ __forceinline__ uint32_t expert(int c) const { return (c * lanes + l) * 8; }
+  uint32_t few;  // a narrow team's lanes
+  int l, t;      // lane within the team, team within the warp
+  __device__ __forceinline__ explicit Team(uint32_t lanes) : few(lanes) {
+    const int lane = threadIdx.x & 31;
+    l = WIDE ? lane : lane & (int)(lanes - 1);
+    t = WIDE ? 0 : lane / (int)lanes;
+  }
+  __device__ __forceinline__ uint32_t lanes() const { return WIDE ? 32 : few; }
+  __device__ __forceinline__ uint32_t per_warp() const { return WIDE ? 1 : 32 / few; }
+  __device__ __forceinline__ uint32_t expert(int c) const { return (c * lanes() + l) * 8; }
   __device__ __forceinline__ float sum(float v) const {
-    for (uint32_t o = 1; o < lanes; o <<= 1) v += __shfl_xor_sync(kAll, v, o);
+    if (WIDE) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    } else {
+      for (uint32_t o = few >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    }
     return v;
   }
   __device__ __forceinline__ float max(float v) const {
-    for (uint32_t o = 1; o < lanes; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    if (WIDE) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    } else {
+      for (uint32_t o = few >> 1; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    }
     return v;
   }
 };
@@ -35,19 +54,12 @@ inline uint32_t team_lanes(uint32_t E) {
   while (n < 32 && n * 8 < E) n *= 2;
   return n;
 }
-__device__ __forceinline__ Team team_here(uint32_t lanes) {
-  const int lane = threadIdx.x & 31;
-  Team t;
-  t.lanes = lanes;
-  t.l = lane & (int)(lanes - 1);
-  t.t = lane / (int)lanes;
-  return t;
-}
 
 // One token's logits; lanes and elements without an expert hold -inf, whose score is 0.
 template <int DT, int NC>
 struct Row {
   Raw8<DT> raw[NC];
+  template <typename Team>
   __device__ __forceinline__ void load(const void *base, size_t ld, uint32_t t, uint32_t E,
                                        const Team &tm, bool vec, bool live) {
     using X = Elem<DT>;
@@ -64,65 +76,127 @@ struct Row {
       }
     }
   }
-  __device__ __forceinline__ void to(float (&l)[NC][8]) const {
+  __device__ __forceinline__ void to(float2 (&l)[NC][4]) const {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      raw[c].to(l[c]);
+      float f[8];
+      raw[c].to(f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) l[c][i] = logit_value(l[c][i]);
+      for (int i = 0; i < 4; ++i) l[c][i] = make_float2(f[2 * i], f[2 * i + 1]);
     }
   }
 };
 
+// arithmetic on two fp32 values an instruction
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+// e^-x for |x| up to 110 (0 at 110, infinite below -88.7): the square of 2^(-x/2 log2 e) by
+// the special function unit, so that a subnormal result is not flushed, with the
+// roundings of the product and of log2 e made good, as those of an argument of 80 would
+// be 80 ulp.  Within 4 ulp.
+__device__ __forceinline__ float2 exp_of_minus(float2 x) {
+  constexpr float kHi = 1.4426950216293335f, kLo = 1.9259629911266175e-8f;  // log2 e
+  constexpr float kLn2 = 0.6931471805599453f;
+  const float2 t = mul2(x, both(-0.5f * kHi));
+  // half of what is missing from the exponent
+  const float2 rest = fma2(x, both(-0.5f * kLo), fma2(x, both(-0.5f * kHi), make_float2(-t.x, -t.y)));
+  float2 e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = fma2(mul2(e, both(kLn2)), rest, e);
+  return mul2(e, e);
+}
+// 1 / x within an ulp; 0 for x above 2^126
+__device__ __forceinline__ float2 rcp2(float2 x) {
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(x.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(x.y));
+  return r;
+}
+
 // l -> scores p (softmax: whose sum is 1), in place; slope = d log p / dl, softmax's
-// without its sum's part.  Returns the sum of p.
-template <int NC, bool SLOPE>
-__device__ __forceinline__ float scores(uint32_t fn, const Team &tm, float (&l)[NC][8],
-                                        float (&slope)[NC][8]) {
-  float s = 0.0f;
+// without its sum's part.  A NaN counts as -inf, +inf as the largest finite value.
+// Returns the sum of p.
+template <int NC, bool SLOPE, typename Team>
+__device__ __forceinline__ float scores(uint32_t fn, const Team &tm, float2 (&l)[NC][4],
+                                        float2 (&slope)[NC][4]) {
+  float2 s = both(0.0f);
   if (fn == MOE_SCORE_SOFTMAX) {
-    float m = -INFINITY;
+    float m = -FLT_MAX;  // of a row of -inf: every term is 0
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, l[c][i]);
+      for (int i = 0; i < 4; ++i) {
+        float2 &v = l[c][i];
+        v.x = fminf(fmaxf(v.x, -INFINITY), FLT_MAX);
+        v.y = fminf(fmaxf(v.y, -INFINITY), FLT_MAX);
+        m = fmaxf(m, fmaxf(v.x, v.y));
+      }
     m = tm.max(m);
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        l[c][i] = softmax_term(l[c][i], m);
-        s += l[c][i];
-        if (SLOPE) slope[c][i] = 1.0f;
+      for (int i = 0; i < 4; ++i) {
+        float2 &v = l[c][i];
+        v = exp_of_minus(make_float2(fminf(m - v.x, 110.0f), fminf(m - v.y, 110.0f)));
+        s = add2(s, v);
+        if (SLOPE) slope[c][i] = both(1.0f);
       }
-    s = tm.sum(s);
-    const float r = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+    const float sum = tm.sum(s.x + s.y);
+    const float r = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) l[c][i] *= r;
-    return s > 0.0f ? 1.0f : 0.0f;
+      for (int i = 0; i < 4; ++i) l[c][i] = mul2(l[c][i], both(r));
+    return sum > 0.0f ? 1.0f : 0.0f;
+  }
+  if (fn == MOE_SCORE_SIGMOID) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = l[c][i];
+        if (SLOPE) {
+          // of e = e^-|l|: 1/(1+e) is the larger of sigmoid(l) and sigmoid(-l), e/(1+e) the other
+          const float2 e = exp_of_minus(
+              make_float2(fminf(fabsf(v.x), 110.0f), fminf(fabsf(v.y), 110.0f)));
+          const float2 big = rcp2(add2(e, both(1.0f))), small = mul2(e, big);
+          const bool ux = v.x >= 0.0f, uy = v.y >= 0.0f;  // NaN: as -inf
+          l[c][i] = make_float2(ux ? big.x : small.x, uy ? big.y : small.y);
+          slope[c][i] = make_float2(ux ? small.x : big.x, uy ? small.y : big.y);
+        } else {
+          const float2 e = exp_of_minus(make_float2(fminf(fmaxf(v.x, -110.0f), 110.0f),
+                                                    fminf(fmaxf(v.y, -110.0f), 110.0f)));
+          l[c][i] = rcp2(add2(e, both(1.0f)));
+        }
+        s = add2(s, l[c][i]);
+      }
+    return tm.sum(s.x + s.y);
   }
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // of e^-|l|: 1/(1+e) is the larger of sigmoid(l) and sigmoid(-l), e/(1+e) the other
-      const float v = l[c][i], e = expf(-fabsf(v));
-      const float big = __frcp_rn(1.0f + e), small = e * big;
-      const float up = v >= 0.0f ? big : small;
-      if (fn == MOE_SCORE_SIGMOID) {
-        l[c][i] = up;
-        if (SLOPE) slope[c][i] = v >= 0.0f ? small : big;
-      } else {
-        const float soft = fmaxf(v, 0.0f) + log1pf(e);
-        l[c][i] = __fsqrt_rn(soft);
+    for (int i = 0; i < 4; ++i) {
+      const float2 e = exp_of_minus(
+          make_float2(fminf(fabsf(l[c][i].x), 110.0f), fminf(fabsf(l[c][i].y), 110.0f)));
+      const float2 big = rcp2(add2(e, both(1.0f))), small = mul2(e, big);
+      auto one = [](float v, float e, float b, float m, float &g) {
+        const float soft = fminf(fmaxf(v, 0.0f), FLT_MAX) + log1pf(e);
         // sigmoid / (2 softplus); 1/2 in the limit of -inf
-        if (SLOPE) slope[c][i] = soft > 0.0f ? __fdiv_rn(0.5f * up, soft) : 0.5f;
-      }
-      s += l[c][i];
+        if (SLOPE) g = soft > 0.0f ? __fdiv_rn(0.5f * (v >= 0.0f ? b : m), soft) : 0.5f;
+        return __fsqrt_rn(soft);
+      };
+      float2 &v = l[c][i], &g = slope[c][i];
+      float gx = 0.0f, gy = 0.0f;
+      v.x = one(v.x, e.x, big.x, small.x, gx);
+      v.y = one(v.y, e.y, big.y, small.y, gy);
+      if (SLOPE) g = make_float2(gx, gy);
+      s = add2(s, v);
     }
-  return tm.sum(s);
+  return tm.sum(s.x + s.y);
 }
 
 // ---------------------------------------------------------------- sequences
@@ -146,8 +220,9 @@ __device__ __forceinline__ uint32_t seq_of(const moe_tokens &t, int x) {
 // before or behind, the sums go to the workspace (the first slot if the sequence begins
 // before the CTA's tokens, the second if it begins among them: at most one each), where
 // k_balance_join adds them in order.
-constexpr uint32_t kSumCtas = 304;  // two an SM, at most
-constexpr uint32_t kSumTokens = 64;  // tokens of a CTA, at least
+constexpr uint32_t kSumCtas = 4;      // an SM, at most (65536 x 256 bf16: 30 us; 34 with 6, 31 with 3)
+constexpr uint32_t kSumPasses = 4;  // tokens of a team, at least
+constexpr uint32_t kJoinRun = 32;   // experts of a joining CTA
 
 struct BalanceArgs {
   RouterGradArgs g;
@@ -158,7 +233,8 @@ struct BalanceArgs {
   float *part;         // [CTAs][2][E] sums of shares
   int32_t *part_count;  // [CTAs][2][E] picks
   int32_t *part_n;      // [CTAs][2] counting tokens
-  float *seq_loss;     // [S]
+  float *seq_loss;     // [S][chunks]: terms of the loss by runs of experts
+  uint32_t chunks;     // runs of kJoinRun experts
   uint32_t *ticket;
 };
 
@@ -176,49 +252,41 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
   return v;
 }
 
-// a sequence's outputs from its sums; n, picks(e) and shares(e) as summed
-template <int THREADS, typename C, typename P>
-__device__ __forceinline__ void finish_sequence(const BalanceArgs &a, uint32_t s, int n, float *red,
-                                                const C &picks, const P &shares) {
-  const uint32_t E = a.g.r.n_expert;
-  float loss = 0.0f;
-  for (uint32_t e = threadIdx.x; e < E; e += THREADS) {
-    const int c = picks(e);
-    const float p = n > 0 ? __fdiv_rn(shares(e), (float)n) : 0.0f;
-    a.count[(size_t)s * E + e] = c;
-    a.prob[(size_t)s * E + e] = p;
-    loss += (float)c * p;
-  }
-  loss = block_sum<THREADS>(loss, red);
-  if (threadIdx.x == 0) {
-    a.tokens[s] = n;
-    a.seq_loss[s] =
-        n > 0 ? loss * __fdiv_rn((float)E, (float)a.g.r.top_k * (float)n) : 0.0f;
-  }
+// a sequence's factor of the loss: E / (k n)
+__device__ __forceinline__ float seq_factor(const BalanceArgs &a, int n) {
+  return n > 0 ? __fdiv_rn((float)a.g.r.n_expert, (float)a.g.r.top_k * (float)n) : 0.0f;
+}
+// one expert's outputs from its sums; returns its term of the loss up to the factor
+__device__ __forceinline__ float finish_expert(const BalanceArgs &a, uint32_t s, uint32_t e, int n,
+                                               int picks, float shares) {
+  const float p = n > 0 ? __fdiv_rn(shares, (float)n) : 0.0f;
+  a.count[(size_t)s * a.g.r.n_expert + e] = picks;
+  a.prob[(size_t)s * a.g.r.n_expert + e] = p;
+  return (float)picks * p;
 }
 
 // the loss from the sequences' terms, by one block
 template <int THREADS>
 __device__ __forceinline__ void finish_loss(const BalanceArgs &a, float *red) {
   float v = 0.0f;
-  for (uint32_t s = threadIdx.x; s < a.g.t.S; s += THREADS) v += __ldcg(a.seq_loss + s);
+  for (uint32_t i = threadIdx.x; i < a.g.t.S * a.chunks; i += THREADS) v += __ldcg(a.seq_loss + i);
   v = block_sum<THREADS>(v, red);
   if (threadIdx.x == 0) a.loss[0] = v * __fdiv_rn(a.g.coef, (float)a.g.t.S);
 }
 
-template <int DT, int NC>
-__global__ void __launch_bounds__(kThreads) k_balance(const BalanceArgs a) {
+template <int DT, int NC, bool WIDE>
+__global__ void __launch_bounds__(kThreads, NC == 1 ? 4 : 2) k_balance(const BalanceArgs a) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ __align__(16) uint8_t bsm[];
   const uint32_t E = a.g.r.n_expert, k = a.g.r.top_k;
-  const uint32_t width = NC * a.lanes * 8;
+  const Team<WIDE> tm(a.lanes);
+  const uint32_t width = NC * tm.lanes() * 8;
   float *red = (float *)bsm;                     // [kWarps][width]
   int *cnt = (int *)(red + kWarps * width);      // [width]
   __shared__ float sums[32];
   __shared__ int live_n;
   const int tid = threadIdx.x, warp = tid >> 5;
-  const Team tm = team_here(a.lanes);
   const bool alone = gridDim.x == 1;
   const int t0 = (int)min(a.g.t.T, blockIdx.x * a.per);
   const int t1 = (int)min((uint64_t)a.g.t.T, (uint64_t)t0 + a.per);
@@ -232,12 +300,20 @@ __global__ void __launch_bounds__(kThreads) k_balance(const BalanceArgs a) {
     for (uint32_t e = tid; e < width; e += kThreads) cnt[e] = 0;
     if (tid == 0) live_n = 0;
     __syncthreads();
+    // the picks of this thread's first token, on the way during the sum of the shares
+    constexpr uint32_t kAhead = 8;
+    const int first = lo + tid;
+    int32_t ahead[kAhead];
+    const bool counting = first < hi && (!a.g.t.live || a.g.t.live[first]);
+#pragma unroll
+    for (uint32_t j = 0; j < kAhead; ++j)
+      ahead[j] = counting && j < k ? a.g.idx[(size_t)first * k + j] : -1;
     // ---- shares
-    float acc[NC][8];
+    float2 acc[NC][4];
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[c][i] = 0.0f;
+      for (int i = 0; i < 4; ++i) acc[c][i] = both(0.0f);
     for (int base = lo + warp * (int)tm.per_warp(); base < hi; base += U * step) {
       Row<DT, NC> row[U];
       bool on[U];
@@ -249,40 +325,52 @@ __global__ void __launch_bounds__(kThreads) k_balance(const BalanceArgs a) {
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        float l[NC][8];
+        float2 l[NC][4];
         row[u].to(l);
         const float sum = scores<NC, false>(a.g.r.score, tm, l, l);
-        const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+        const float inv = on[u] && sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[c][i] = __fmaf_rn(l[c][i], inv, acc[c][i]);
+          for (int i = 0; i < 4; ++i) acc[c][i] = fma2(l[c][i], both(inv), acc[c][i]);
       }
     }
-    // ---- picks
-    int mine = 0;
-    if (a.g.t.live)
-      for (int t = lo + tid; t < hi; t += kThreads) mine += a.g.t.live[t] != 0;
-    else if (tid == 0)
-      mine = max(hi - lo, 0);
-    if (mine) atomicAdd(&live_n, mine);
-    const uint32_t i1 = (uint32_t)max(hi, lo) * k;
-#pragma unroll 4
-    for (uint32_t i = (uint32_t)lo * k + tid; i < i1; i += kThreads) {
-      const uint32_t e = (uint32_t)a.g.idx[i];
-      if (e < E && (!a.g.t.live || a.g.t.live[i / k])) atomicAdd(&cnt[e], 1);
+    // ---- picks, a thread a token
+    int mine = counting;
+#pragma unroll
+    for (uint32_t j = 0; j < kAhead; ++j)
+      if ((uint32_t)ahead[j] < E) atomicAdd(&cnt[ahead[j]], 1);
+    for (int t = first; t < hi; t += kThreads) {
+      uint32_t j = 0;
+      if (t == first) {
+        if (!counting) continue;
+        j = kAhead;
+      } else {
+        if (a.g.t.live && !a.g.t.live[t]) continue;
+        ++mine;
+      }
+      for (; j < k; ++j) {
+        const uint32_t e = (uint32_t)a.g.idx[(size_t)t * k + j];
+        if (e < E) atomicAdd(&cnt[e], 1);
+      }
     }
+    mine = __reduce_add_sync(kAll, mine);
+    if (mine && (tid & 31) == 0) atomicAdd(&live_n, mine);
     // ---- the warps' shares in order
-    for (uint32_t o = tm.lanes; o < 32; o <<= 1)
+    for (uint32_t o = tm.lanes(); o < 32; o <<= 1)
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[c][i] += __shfl_xor_sync(kAll, acc[c][i], o);
+        for (int i = 0; i < 4; ++i) {
+          acc[c][i].x += __shfl_xor_sync(kAll, acc[c][i].x, o);
+          acc[c][i].y += __shfl_xor_sync(kAll, acc[c][i].y, o);
+        }
     if (tm.t == 0)
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) red[warp * width + tm.expert(c) + i] = acc[c][i];
+        for (int i = 0; i < 4; ++i)
+          *(float2 *)(red + warp * width + tm.expert(c) + 2 * i) = acc[c][i];
     __syncthreads();
     auto shares = [&](uint32_t e) {
       float v = 0.0f;
@@ -291,7 +379,14 @@ __global__ void __launch_bounds__(kThreads) k_balance(const BalanceArgs a) {
       return v;
     };
     if (s0 >= t0 && s1 <= t1) {
-      finish_sequence<kThreads>(a, s, live_n, sums, [&](uint32_t e) { return cnt[e]; }, shares);
+      const int n = live_n;
+      float loss = 0.0f;
+      for (uint32_t e = tid; e < E; e += kThreads)
+        loss += finish_expert(a, s, e, n, cnt[e], shares(e));
+      loss = block_sum<kThreads>(loss, sums);
+      if (tid == 0) a.tokens[s] = n;
+      if ((uint32_t)tid < a.chunks)
+        a.seq_loss[s * a.chunks + tid] = tid == 0 ? loss * seq_factor(a, n) : 0.0f;
     } else {
       const size_t slot = blockIdx.x * 2 + (s0 >= t0);
       for (uint32_t e = tid; e < E; e += kThreads) {
@@ -311,70 +406,61 @@ __global__ void __launch_bounds__(kThreads) k_balance(const BalanceArgs a) {
 
 constexpr int kJoinThreads = 512;
 
-// the sequences that no CTA had to itself, empty ones, and the loss
+// The sequences that no CTA had to itself, empty ones, and the loss.  A CTA joins a run of
+// 32 experts of a sequence, a warp every 16th of its parts; the last one adds up the loss.
 __global__ void __launch_bounds__(kJoinThreads) k_balance_join(const BalanceArgs a) {
   pdl_trigger();
   pdl_wait();
+  constexpr int kGroups = kJoinThreads / (int)kJoinRun;
   __shared__ float sums[32];
-  __shared__ float share_g[kJoinThreads];
-  __shared__ int count_g[kJoinThreads];
+  __shared__ float share_g[kGroups][kJoinRun];
+  __shared__ int count_g[kGroups][kJoinRun];
   __shared__ int live_n;
   __shared__ bool last;
   const uint32_t E = a.g.r.n_expert;
-  const int tid = threadIdx.x;
-  for (uint32_t s = blockIdx.x; s < a.g.t.S; s += gridDim.x) {
+  const int tid = threadIdx.x, g = tid / (int)kJoinRun, l = tid % (int)kJoinRun;
+  const uint32_t items = a.g.t.S * a.chunks;
+  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const uint32_t s = item / a.chunks, chunk = item - s * a.chunks, e = chunk * kJoinRun + l;
     const int s0 = seq_at(a.g.t, s), s1 = seq_at(a.g.t, s + 1);
-    if (s0 >= s1) {
-      finish_sequence<kJoinThreads>(a, s, 0, sums, [](uint32_t) { return 0; },
-                                    [](uint32_t) { return 0.0f; });
-      continue;
-    }
-    const uint32_t c0 = (uint32_t)s0 / a.per, c1 = (uint32_t)(s1 - 1) / a.per;
-    if (c0 == c1) continue;
+    const uint32_t c0 = (uint32_t)s0 / a.per, c1 = s0 < s1 ? (uint32_t)(s1 - 1) / a.per : c0;
+    if (s0 < s1 && c0 == c1) continue;  // its CTA has written it
     // the sequence begins among the tokens of c0
     auto slot = [&](uint32_t c) { return (size_t)c * 2 + ((uint32_t)s0 >= c * a.per); };
+    __syncthreads();
     if (tid == 0) live_n = 0;
     __syncthreads();
-    int n = 0;
-    for (uint32_t c = c0 + tid; c <= c1; c += kJoinThreads) n += __ldcg(a.part_n + slot(c));
-    if (n) atomicAdd(&live_n, n);
-    __syncthreads();
-    n = live_n;
-    // groups of threads share the CTAs, for a run of experts at a time
-    const uint32_t run = E < (uint32_t)kJoinThreads ? E : (uint32_t)kJoinThreads;
-    const uint32_t groups = kJoinThreads / run;
-    float loss = 0.0f;
-    for (uint32_t e0 = 0; e0 < E; e0 += run) {
-      const uint32_t g = tid / run, e = e0 + tid - g * run;
-      float v = 0.0f;
-      int c_sum = 0;
-      if (g < groups && e < E) {
+    int n = 0, picks = 0;
+    float v = 0.0f;
+    if (s0 < s1) {
+      for (uint32_t c = c0 + tid; c <= c1; c += kJoinThreads) n += __ldcg(a.part_n + slot(c));
+      if (n) atomicAdd(&live_n, n);
+      if (e < E)
 #pragma unroll 8
-        for (uint32_t c = c0 + g; c <= c1; c += groups) {
+        for (uint32_t c = c0 + g; c <= c1; c += kGroups) {
           v += __ldcg(a.part + slot(c) * E + e);
-          c_sum += __ldcg(a.part_count + slot(c) * E + e);
+          picks += __ldcg(a.part_count + slot(c) * E + e);
         }
-      }
-      __syncthreads();
-      share_g[tid] = v;
-      count_g[tid] = c_sum;
-      __syncthreads();
-      if (g == 0 && e < E) {
-        for (uint32_t q = 1; q < groups; ++q) {
-          v += share_g[q * run + tid];
-          c_sum += count_g[q * run + tid];
-        }
-        const float p = n > 0 ? __fdiv_rn(v, (float)n) : 0.0f;
-        a.count[(size_t)s * E + e] = c_sum;
-        a.prob[(size_t)s * E + e] = p;
-        loss += (float)c_sum * p;
-      }
     }
-    loss = block_sum<kJoinThreads>(loss, sums);
-    if (tid == 0) {
-      a.tokens[s] = n;
-      a.seq_loss[s] =
-          n > 0 ? loss * __fdiv_rn((float)E, (float)a.g.r.top_k * (float)n) : 0.0f;
+    share_g[g][l] = v;
+    count_g[g][l] = picks;
+    __syncthreads();
+    if (g == 0) {
+      n = live_n;
+      v = 0.0f;
+      picks = 0;
+#pragma unroll
+      for (int q = 0; q < kGroups; ++q) {
+        v += share_g[q][l];
+        picks += count_g[q][l];
+      }
+      float loss = e < E ? finish_expert(a, s, e, n, picks, v) : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(kAll, loss, o);
+      if (l == 0) {
+        a.seq_loss[item] = loss * seq_factor(a, n);
+        if (chunk == 0) a.tokens[s] = n;
+      }
     }
   }
   __threadfence();
@@ -402,115 +488,159 @@ struct RouteBackArgs {
   size_t ldd;
 };
 
-template <int OT, int NC>
+template <int OT, int NC, typename Team>
 __device__ __forceinline__ void store_row(const RouteBackArgs &a, uint32_t t, const Team &tm,
-                                          const float (&d)[NC][8]) {
+                                          const float2 (&d2)[NC][4]) {
   typename Elem<OT>::T *row = (typename Elem<OT>::T *)a.dlogits + (size_t)t * a.ldd;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const uint32_t e = tm.expert(c);
+    const float d[8] = {d2[c][0].x, d2[c][0].y, d2[c][1].x, d2[c][1].y,
+                        d2[c][2].x, d2[c][2].y, d2[c][3].x, d2[c][3].y};
     if (a.vec_out) {
-      if (e < a.g.r.n_expert) store8<OT>(row + e, d[c]);
+      if (e < a.g.r.n_expert) store8<OT>(row + e, d);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (e + i < a.g.r.n_expert) row[e + i] = Elem<OT>::from(d[c][i]);
+        if (e + i < a.g.r.n_expert) row[e + i] = Elem<OT>::from(d[i]);
     }
   }
 }
 
-// A warp takes `run` consecutive groups of tokens, the next one's logits on the way while
-// it works on one.  The picks' part goes through shared memory: p is laid out there
-// for the picks' lanes to fetch, then the gradient, to which they add.
-template <int DT, int NC>
-__global__ void __launch_bounds__(kThreads) k_route_backward(const RouteBackArgs a) {
+// A warp takes `run` consecutive groups of tokens, the next one's logits and picks on the way
+// while it works on one; the loss's coefficients of a sequence's experts stay in registers
+// from token to token.  The picks' part goes through shared memory: p is laid out there for
+// the picks' lanes to fetch; they add theirs to a row of zeros, which every lane collects.
+template <int DT, int NC, bool WIDE>
+__global__ void __launch_bounds__(kThreads, NC == 1 ? kBackCtas : NC == 2 ? 2 : 1)
+    k_route_backward(const RouteBackArgs a) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ __align__(16) uint8_t rsm[];
   const uint32_t E = a.g.r.n_expert, k = a.g.r.top_k, fn = a.g.r.score;
-  const Team tm = team_here(a.lanes);
-  const uint32_t width = NC * a.lanes * 8, nt = tm.per_warp();
-  float *buf = (float *)rsm + ((size_t)(threadIdx.x >> 5) * nt + tm.t) * width;  // the team's
-  const uint64_t g0 = ((uint64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * a.run;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Team<WIDE> tm(a.lanes);
+  constexpr uint32_t kRounds = WIDE ? 1 : 8;
+  const uint32_t width = NC * tm.lanes() * 8, nt = tm.per_warp();
+  float *pbuf = (float *)rsm + ((size_t)warp * nt + tm.t) * 2 * width;  // the team's scores
+  float *vbuf = pbuf + width;                                          // ... and zeros
+  const uint64_t g0 = ((uint64_t)blockIdx.x * kWarps + warp) * a.run;
   const uint64_t groups = ((uint64_t)a.g.t.T + nt - 1) / nt;
   if (g0 >= groups) return;
   const uint32_t n_groups = (uint32_t)min((uint64_t)a.run, groups - g0);
   uint32_t t = (uint32_t)(g0 * nt) + tm.t;
   const bool softmax = fn == MOE_SCORE_SOFTMAX;
+  auto put = [&](float *buf, const float2 (&v)[NC][4]) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      float4 *b = (float4 *)(buf + tm.expert(c));
+      b[0] = make_float4(v[c][0].x, v[c][0].y, v[c][1].x, v[c][1].y);
+      b[1] = make_float4(v[c][2].x, v[c][2].y, v[c][3].x, v[c][3].y);
+    }
+  };
   // factor of a sequence's loss gradient, up to 1 / n^2
   const float factor =
       a.count ? (a.dloss ? a.dloss[0] : 1.0f) *
                     __fdiv_rn(a.g.coef * (float)E, (float)a.g.t.S * (float)k)
               : 0.0f;
   uint32_t s = a.count ? seq_of(a.g.t, (int)t) : 0;
-  int s_end = a.count && s < a.g.t.S ? seq_at(a.g.t, s + 1) : 0;
+  int s_begin = 0, s_end = 0;
+  uint32_t have = 0xffffffffu;  // the sequence whose coefficients coef holds
+  float2 coef[NC][4];
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) coef[c][j] = both(0.0f);
+  if (a.dw) put(vbuf, coef);
+  if (a.count && s < a.g.t.S) {
+    s_begin = seq_at(a.g.t, s);
+    s_end = seq_at(a.g.t, s + 1);
+  }
+  // slots of this lane: l, l + lanes, ...
+  const uint32_t rounds = WIDE ? 1 : (k + tm.lanes() - 1) / tm.lanes();  // 8 at most: k <= E
   Row<DT, NC> next;
-  next.load(a.g.logits, a.g.ld, t, E, tm, a.vec, t < a.g.t.T);
+  uint32_t next_e = E;  // the first slot's pick and gradient
+  float next_g = 0.0f;
+  bool next_live = true;
+  auto fetch = [&](uint32_t x) {
+    const bool in = x < a.g.t.T;
+    next.load(a.g.logits, a.g.ld, x, E, tm, a.vec, in);
+    if (a.dw) {
+      const bool mine = in && (uint32_t)tm.l < k;
+      next_e = mine ? min((uint32_t)a.g.idx[(size_t)x * k + tm.l], E) : E;
+      next_g = mine ? a.dw[(size_t)x * k + tm.l] : 0.0f;
+    }
+    if (a.count && a.g.t.live) next_live = in && a.g.t.live[x];
+  };
+  fetch(t);
   for (uint32_t i = 0; i < n_groups; ++i, t += nt) {
-    const bool on = t < a.g.t.T;
-    float p[NC][8], slope[NC][8];
+    const bool on = t < a.g.t.T, live = next_live;
+    const uint32_t e0 = next_e;
+    const float w0 = next_g;
+    float2 p[NC][4], slope[NC][4], d[NC][4];
     next.to(p);
-    if (i + 1 < n_groups)
-      next.load(a.g.logits, a.g.ld, t + nt, E, tm, a.vec, t + nt < a.g.t.T);
+    if (i + 1 < n_groups) fetch(t + nt);
     const float sum = scores<NC, true>(fn, tm, p, slope);
-    float d[NC][8];
     // ---- the loss's part
     bool counts = false;
     if (a.count && on) {
       while (s < a.g.t.S && s_end <= (int)t) {
         ++s;
-        if (s < a.g.t.S) s_end = seq_at(a.g.t, s + 1);
+        if (s < a.g.t.S) {
+          s_begin = seq_at(a.g.t, s);
+          s_end = seq_at(a.g.t, s + 1);
+        }
       }
-      counts = s < a.g.t.S && seq_at(a.g.t, s) <= (int)t && (!a.g.t.live || a.g.t.live[t]);
+      counts = s < a.g.t.S && s_begin <= (int)t && live;
+      if (counts && s != have) {
+        const int32_t *cs = a.count + (size_t)s * E;
+        const float n = (float)max(a.tokens[s], 1), f = __fdiv_rn(factor, n * n);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t e = tm.expert(c) + 2 * j;
+            coef[c][j] = make_float2(e < E ? f * (float)cs[e] : 0.0f,
+                                     e + 1 < E ? f * (float)cs[e + 1] : 0.0f);
+          }
+        have = s;
+      }
     }
     if (__any_sync(kAll, counts)) {
-      const int32_t *cs = a.count + (size_t)min(s, a.g.t.S - 1) * E;
-      const float n = counts ? (float)max(a.tokens[s], 1) : 1.0f;
-      const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-      const float f = counts ? __fdiv_rn(factor, n * n) : 0.0f;
-      float dot = 0.0f;
+      const float inv = counts && sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+      float2 dots = both(0.0f);
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t e = tm.expert(c) + j;
-          d[c][j] = e < E ? f * (float)cs[e] : 0.0f;
-          dot = __fmaf_rn(d[c][j], p[c][j] * inv, dot);
-        }
-      dot = tm.sum(dot);
+        for (int j = 0; j < 4; ++j) dots = fma2(coef[c][j], p[c][j], dots);
+      const float dot = tm.sum(dots.x + dots.y) * inv;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[c][j] = p[c][j] * inv * (d[c][j] - dot);
+        for (int j = 0; j < 4; ++j)
+          d[c][j] = mul2(mul2(p[c][j], both(inv)), add2(coef[c][j], both(-dot)));
     } else {
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[c][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) d[c][j] = both(0.0f);
     }
     // ---- the picks' part
     if (a.dw) {
-      auto put = [&](const float (&v)[NC][8]) {
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          float4 *b = (float4 *)(buf + tm.expert(c));
-          b[0] = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
-          b[1] = make_float4(v[c][4], v[c][5], v[c][6], v[c][7]);
-        }
-      };
-      auto pick = [&](uint32_t j) {  // expert of slot j, E if it is none
-        return on ? min((uint32_t)a.g.idx[(size_t)t * k + j], E) : E;
-      };
+      put(pbuf, p);
       __syncwarp();
-      put(p);
-      __syncwarp();
+      float pk[kRounds], gk[kRounds];  // of this lane's slots: p and dw, 0 where there is none
+      uint32_t ek[kRounds];
       float total = 0.0f, dots = 0.0f;
-      for (uint32_t j = tm.l; j < k; j += tm.lanes) {
-        const uint32_t e = pick(j);
-        if (e < E) {
-          total += buf[e];
-          dots = __fmaf_rn(buf[e], a.dw[(size_t)t * k + j], dots);
-        }
+#pragma unroll
+      for (uint32_t m = 0; m < kRounds; ++m) {
+        if (m >= rounds) break;
+        const uint32_t j = tm.l + m * tm.lanes();
+        ek[m] = m == 0 ? e0 : on && j < k ? min((uint32_t)a.g.idx[(size_t)t * k + j], E) : E;
+        gk[m] = m == 0 ? w0 : ek[m] < E ? a.dw[(size_t)t * k + j] : 0.0f;
+        pk[m] = ek[m] < E ? pbuf[ek[m]] : 0.0f;
+        total += pk[m];
+        dots = __fmaf_rn(pk[m], ek[m] < E ? gk[m] : 0.0f, dots);
       }
       total = tm.sum(total);
       dots = tm.sum(dots);
@@ -519,55 +649,43 @@ __global__ void __launch_bounds__(kThreads) k_route_backward(const RouteBackArgs
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) d[c][j] = __fmaf_rn(-a.g.r.s * dots, p[c][j], d[c][j]);
+          for (int j = 0; j < 4; ++j) d[c][j] = fma2(both(-a.g.r.s * dots), p[c][j], d[c][j]);
       }
-      // the slots in order, a round of the team's lanes at a time: a lane's own part...
-      const uint32_t rounds = (k + tm.lanes - 1) / tm.lanes;
-      float pk[8];  // p of this lane's picks: k <= E <= 8 lanes (256 for 32 lanes: k <= 32)
 #pragma unroll
-      for (uint32_t m = 0; m < 8; ++m) {
-        const uint32_t j = tm.l + m * tm.lanes;
-        pk[m] = 0.0f;
-        if (m < rounds && j < k) {
-          const uint32_t e = pick(j);
-          if (e < E) pk[m] = buf[e];
-        }
-      }
-      __syncwarp();
-      put(d);
-      __syncwarp();
-#pragma unroll
-      for (uint32_t m = 0; m < 8; ++m) {
+      for (uint32_t m = 0; m < kRounds; ++m) {
         if (m >= rounds) break;
-        const uint32_t j = tm.l + m * tm.lanes;
-        const uint32_t e = j < k ? pick(j) : E;
-        float v = 0.0f;
-        if (e < E) {
-          const float g = a.dw[(size_t)t * k + j];
-          v = a.g.r.renorm ? a.g.r.s * (pk[m] * inv) * (g - dots * inv) : a.g.r.s * pk[m] * g;
-        }
-        // ...and the lanes one after another where two of them have the same expert
-        const uint32_t key = e < E ? (uint32_t)tm.t * 1024 + e : 0x80000000u + (threadIdx.x & 31);
+        const uint32_t e = ek[m];
+        const float v = a.g.r.renorm ? a.g.r.s * (pk[m] * inv) * (gk[m] - dots * inv)
+                                     : a.g.r.s * pk[m] * gk[m];
+        // the lanes one after another where two of them have the same expert
+        const uint32_t key = e < E ? (uint32_t)tm.t * 1024 + e : 0x80000000u + (uint32_t)lane;
         const uint32_t same = __match_any_sync(kAll, key);
-        uint32_t before = __popc(same & ((1u << (threadIdx.x & 31)) - 1u));
+        const uint32_t before = __popc(same & ((1u << lane) - 1u));
         for (uint32_t turn = 0; __any_sync(kAll, before >= turn); ++turn) {
-          if (before == turn && e < E) buf[e] += v;
+          if (before == turn && e < E) vbuf[e] += v;
           __syncwarp();
         }
       }
-      __syncwarp();
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const float4 *b = (const float4 *)(buf + tm.expert(c));
+        const float4 *b = (const float4 *)(vbuf + tm.expert(c));
         const float4 x = b[0], y = b[1];
-        d[c][0] = x.x, d[c][1] = x.y, d[c][2] = x.z, d[c][3] = x.w;
-        d[c][4] = y.x, d[c][5] = y.y, d[c][6] = y.z, d[c][7] = y.w;
+        d[c][0] = add2(d[c][0], make_float2(x.x, x.y));
+        d[c][1] = add2(d[c][1], make_float2(x.z, x.w));
+        d[c][2] = add2(d[c][2], make_float2(y.x, y.y));
+        d[c][3] = add2(d[c][3], make_float2(y.z, y.w));
+      }
+      __syncwarp();
+#pragma unroll
+      for (uint32_t m = 0; m < kRounds; ++m) {
+        if (m >= rounds) break;
+        if (ek[m] < E) vbuf[ek[m]] = 0.0f;
       }
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[c][j] *= slope[c][j];
+      for (int j = 0; j < 4; ++j) d[c][j] = mul2(d[c][j], slope[c][j]);
     if (!on) continue;
     if (a.odt == MOE_DT_F32) store_row<MOE_DT_F32, NC>(a, t, tm, d);
     else if (a.odt == MOE_DT_BF16) store_row<MOE_DT_BF16, NC>(a, t, tm, d);
@@ -600,14 +718,13 @@ __global__ void __launch_bounds__(kThreads) k_combine_backward(const CombineBack
   using X = Elem<DT>;
   using Y = Elem<YT>;
   const int lane = threadIdx.x & 31;
-  const uint64_t items = (uint64_t)a.T * a.k;
-  for (uint64_t it = (uint64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); it < items;
-       it += (uint64_t)gridDim.x * kWarps) {
-    const uint32_t t = (uint32_t)(it / a.k);
+  const uint32_t it = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (it < a.T * a.k) {
+    const uint32_t t = it / a.k;
     const uint32_t r = (uint32_t)a.pos[it];
     if (r >= a.R) {
       if (a.dw && lane == 0) a.dw[it] = 0.0f;
-      continue;
+      return;
     }
     const typename Y::T *y = (const typename Y::T *)a.dy + (size_t)t * a.ldy;
     const typename X::T *o = (const typename X::T *)a.o + (size_t)r * a.ldo;
@@ -665,25 +782,29 @@ template <int DT>
 cudaError_t balance_t(const BalanceArgs &a, unsigned grid, cudaStream_t stream) {
   const int nc = chunks_of(a.g.r.n_expert);
   const size_t smem = (size_t)(kWarps + 1) * nc * a.lanes * 8 * 4;
-  if (nc == 1) return launch_k(k_balance<DT, 1>, grid, kThreads, smem, stream, true, a);
-  if (nc == 2) return launch_k(k_balance<DT, 2>, grid, kThreads, smem, stream, true, a);
-  return launch_k(k_balance<DT, 4>, grid, kThreads, smem, stream, true, a);
+  if (a.lanes < 32) return launch_k(k_balance<DT, 1, false>, grid, kThreads, smem, stream, true, a);
+  if (nc == 1) return launch_k(k_balance<DT, 1, true>, grid, kThreads, smem, stream, true, a);
+  if (nc == 2) return launch_k(k_balance<DT, 2, true>, grid, kThreads, smem, stream, true, a);
+  return launch_k(k_balance<DT, 4, true>, grid, kThreads, smem, stream, true, a);
 }
 
 template <int DT>
 cudaError_t route_backward_t(const RouteBackArgs &a, unsigned grid, cudaStream_t stream) {
   const int nc = chunks_of(a.g.r.n_expert);
-  const size_t smem = (size_t)kWarps * 32 / a.lanes * nc * a.lanes * 8 * 4;
-  if (nc == 1) return launch_k(k_route_backward<DT, 1>, grid, kThreads, smem, stream, true, a);
-  if (nc == 2) return launch_k(k_route_backward<DT, 2>, grid, kThreads, smem, stream, true, a);
-  return launch_k(k_route_backward<DT, 4>, grid, kThreads, smem, stream, true, a);
+  const size_t smem = (size_t)kWarps * 32 * nc * 8 * 4 * 2;
+  if (a.lanes < 32) return launch_k(k_route_backward<DT, 1, false>, grid, kThreads, smem, stream, true, a);
+  if (nc == 1) return launch_k(k_route_backward<DT, 1, true>, grid, kThreads, smem, stream, true, a);
+  if (nc == 2) return launch_k(k_route_backward<DT, 2, true>, grid, kThreads, smem, stream, true, a);
+  static std::atomic<bool> done[kMaxDevices];
+  const cudaError_t e = allow_smem(k_route_backward<DT, 4, true>, done);
+  if (e != cudaSuccess) return e;
+  return launch_k(k_route_backward<DT, 4, true>, grid, kThreads, smem, stream, true, a);
 }
 
 template <int DT, int YT>
 cudaError_t combine_backward_t(const CombineBackArgs &a, cudaStream_t stream) {
-  const uint64_t items = (uint64_t)a.T * a.k, most = (uint64_t)fp8_ctas() * 8;
-  const uint64_t need = (items + kWarps - 1) / kWarps;
-  const unsigned grid = (unsigned)(need < most ? need : most);
+  // below 2^27, as the host checked
+  const unsigned grid = (unsigned)(((uint64_t)a.T * a.k + kWarps - 1) / kWarps);
   const bool vec = a.d % 8 == 0 && vec_rows(a.dy, YT, a.ldy) && (!a.dw || vec_rows(a.o, DT, a.ldo)) &&
                    (!a.dout || vec_rows(a.dout, DT, a.ldd));
   return launch_k(vec ? k_combine_backward<DT, YT, true> : k_combine_backward<DT, YT, false>, grid,
@@ -697,24 +818,26 @@ cudaError_t combine_backward_from(int ydt, const CombineBackArgs &a, cudaStream_
   return combine_backward_t<DT, MOE_DT_F16>(a, stream);
 }
 
-uint32_t balance_ctas(uint32_t T) {
-  const uint32_t n = (T + kSumTokens - 1) / kSumTokens;
-  return n < 1 ? 1 : n < kSumCtas ? n : kSumCtas;
+uint32_t balance_ctas(uint32_t T, uint32_t E) {
+  const uint32_t least = kWarps * (32 / team_lanes(E)) * kSumPasses;  // tokens of a CTA
+  const uint32_t n = (T + least - 1) / least, most = kSumCtas * (uint32_t)fp8_ctas();
+  return n < 1 ? 1 : n < most ? n : most;
 }
 
 }  // namespace
 
 size_t balance_ws(const moe_router &r, uint32_t T, uint32_t S) {
-  const size_t n = balance_ctas(T);
-  return MOE_WS_FIXED_BYTES + 4 * (n * 2 * (2 * (size_t)r.n_expert + 1) + S);
+  const size_t n = balance_ctas(T, r.n_expert), chunks = (r.n_expert + kJoinRun - 1) / kJoinRun;
+  return MOE_WS_FIXED_BYTES + 4 * (n * 2 * (2 * (size_t)r.n_expert + 1) + S * chunks);
 }
 
 cudaError_t launch_balance(const RouterGradArgs &g, int32_t *count, int32_t *tokens, float *prob,
                            float *loss, void *ws, cudaStream_t stream) {
   BalanceArgs a;
   a.g = g;
-  const uint32_t E = g.r.n_expert, n = balance_ctas(g.t.T);
+  const uint32_t E = g.r.n_expert, n = balance_ctas(g.t.T, E);
   a.lanes = team_lanes(E);
+  a.chunks = (E + kJoinRun - 1) / kJoinRun;
   a.per = (g.t.T + n - 1) / n;
   if (a.per == 0) a.per = 1;
   a.vec = E % 8 == 0 && vec_rows(g.logits, g.dt, g.ld);
@@ -731,8 +854,8 @@ cudaError_t launch_balance(const RouterGradArgs &g, int32_t *count, int32_t *tok
                   : g.dt == MOE_DT_BF16 ? balance_t<MOE_DT_BF16>(a, n, stream)
                                         : balance_t<MOE_DT_F16>(a, n, stream);
   if (e != cudaSuccess || n == 1) return e;
-  const uint32_t most = 4 * (uint32_t)fp8_ctas();
-  return launch_k(k_balance_join, g.t.S < most ? g.t.S : most, kJoinThreads, 0, stream, true, a);
+  const uint32_t most = 4 * (uint32_t)fp8_ctas(), items = g.t.S * a.chunks;
+  return launch_k(k_balance_join, items < most ? items : most, kJoinThreads, 0, stream, true, a);
 }
 
 cudaError_t launch_route_backward(const RouterGradArgs &g, const float *dw, const int32_t *count,
@@ -751,7 +874,7 @@ cudaError_t launch_route_backward(const RouterGradArgs &g, const float *dw, cons
   a.odt = odt;
   a.ldd = ldd;
   const uint64_t groups = ((uint64_t)g.t.T + 32 / a.lanes - 1) / (32 / a.lanes);
-  const uint64_t warps = (uint64_t)fp8_ctas() * 4 * kWarps;
+  const uint64_t warps = (uint64_t)fp8_ctas() * kBackCtas * kWarps;
   a.run = (uint32_t)((groups + warps - 1) / warps);
   const unsigned grid = (unsigned)((groups + (uint64_t)a.run * kWarps - 1) / ((uint64_t)a.run * kWarps));
   if (g.dt == MOE_DT_F32) return route_backward_t<MOE_DT_F32>(a, grid, stream);
