@@ -24,6 +24,8 @@ struct Int8Call {
 };
 size_t int8_gemm_ws(uint32_t rows);
 cudaError_t launch_int8_gemm(const Int8Call &c);
+// the same of a few rows in all on CUDA cores (int8_few.cu), same conditions
+cudaError_t launch_int8_few(Fp8Args &a, bool swiglu, cudaStream_t stream);
 // the tensor-core products (int8_tc.cu): operands that tensor copies can take
 bool int8_tc_ok(const Fp8Args &a);
 size_t int8_tc_ws(uint32_t rows);

@@ -103,6 +103,19 @@ cudaError_t run_core(Fp8Args &a, cudaStream_t stream) {
   return launch_k(kern, 4 * fp8_ctas(), kCoreThreads, smem, stream, true, a);
 }
 
+// The stream kernel for few rows takes calls whose rows have about an expert each (or no more
+// than four in all) and whose activations fit a CTA's shared memory; the tensor-core kernel
+// those whose experts have several.  Top 8 of 256, d 6144, f 2048, us, stream and tensor-core:
+//   tokens           1         2         4         8        16        24
+//   gate/up    36   43   60   70  104  114  180  201  275  298  376  391
+//   down       21   26   36   39   60   63  100  108              118  115 (K 1024)
+// 64 and 128 rows of 16 experts (gate/up): 77 and 72, 120 and 79; 16 of 4: 28 and 24; one
+// expert, K 6144: 4 rows 11.2 and 14.1, 8 rows (gate/up) 12 and 15, 12 rows 19 and 16; K 1024,
+// 8 rows: 12 and 7.
+bool few_rows(const Fp8Args &a) {
+  return 2ull * a.R <= (a.E > 8 ? a.E : 8) && (uint64_t)a.n_x * a.K <= 200 * 1024;
+}
+
 }  // namespace
 
 size_t int8_gemm_ws(uint32_t rows) {
@@ -133,7 +146,9 @@ cudaError_t launch_int8_gemm(const Int8Call &c) {
   a.err = (uint32_t *)c.ws;
   a.sync = (uint32_t *)(c.ws + 256) + kFp8TileSync;
   a.part = (float *)(c.ws + MOE_WS_FIXED_BYTES);
-  if (int8_tc_ok(a)) return launch_int8_tc(a, c.swiglu, c.stream);
+  if (int8_tc_ok(a))
+    return few_rows(a) ? launch_int8_few(a, c.swiglu, c.stream)
+                       : launch_int8_tc(a, c.swiglu, c.stream);
   return c.swiglu ? run_core<true>(a, c.stream) : run_core<false>(a, c.stream);
 }
 
