@@ -58,10 +58,11 @@ struct RowTiles {
   int total;
 };
 
-// called by all threads; sm: 2(E+1) + 1 ints.  One warp does it, a run of experts a
-// lane, behind a single block barrier: it is on every call's critical path.
+// called by all threads; sm: 2(E+1) + 1 ints; mt: rows of a tile, if fewer than MT.  One warp
+// does it, a run of experts a lane, behind a single block barrier: it is on every call's
+// critical path.
 template <int MT>
-__device__ __forceinline__ RowTiles fp8_row_tiles(const Fp8Args &a, int *sm) {
+__device__ __forceinline__ RowTiles fp8_row_tiles(const Fp8Args &a, int *sm, int mt = MT) {
   int *s_off = sm, *s_tile = sm + (a.E + 1), *s_total = s_tile + (a.E + 1);
   const int E = (int)a.E, R = (int)a.R;
   if (threadIdx.x < 32) {
@@ -88,7 +89,7 @@ __device__ __forceinline__ RowTiles fp8_row_tiles(const Fp8Args &a, int *sm) {
         if (b + i < e1) {
           s_off[b + i] = at;
           bad |= next[i] < at || next[i] > R;
-          tiles += (max(next[i] - at, 0) + MT - 1) / MT;
+          tiles += (max(next[i] - at, 0) + mt - 1) / mt;
           at = next[i];
         }
       }
@@ -103,7 +104,7 @@ __device__ __forceinline__ RowTiles fp8_row_tiles(const Fp8Args &a, int *sm) {
         s_off[e] = at;
         s_tile[e] = tiles;  // within the lane's run so far
         bad |= next < at || next > R;
-        tiles += (max(next - at, 0) + MT - 1) / MT;
+        tiles += (max(next - at, 0) + mt - 1) / mt;
         at = next;
       }
       incl = warp_scan(tiles);
@@ -132,7 +133,8 @@ struct Fp8Tile {
 // By a whole warp: tile v of total * n_tiles: experts in order, an expert's column tiles one
 // after another, its row tiles innermost (they share the weights)
 template <int MT>
-__device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Args &a, const RowTiles &rt, int v) {
+__device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Args &a, const RowTiles &rt, int v,
+                                            int tile_rows = MT) {
   // expert e's tiles are [tile[e] * n_tiles, tile[e+1] * n_tiles)
   const int q = (int)quotient((uint32_t)v, a.n_tiles, a.n_tiles_inv);
   // the largest e with tile[e] <= q (experts without rows share a prefix): a run of
@@ -149,8 +151,8 @@ __device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Args &a, const RowTiles &rt
   t.e = lo;
   t.nt = mt == 1 ? local : local / mt;
   const int m = local - t.nt * mt;
-  t.row0 = rt.off[lo] + m * MT;
-  t.rows = min(MT, rt.off[lo + 1] - t.row0);
+  t.row0 = rt.off[lo] + m * tile_rows;
+  t.rows = min(tile_rows, rt.off[lo + 1] - t.row0);
   return t;
 }
 

@@ -44,19 +44,25 @@
 namespace moe {
 namespace {
 
+constexpr uint32_t kRing = 12;    // stages of a ring, at most
+constexpr uint32_t kCtrl = 1024;  // bytes for barriers
+static_assert((2 * kMaxStages + 2 * kRing + 2 * 8 + 2) * 8 + 12 <= kCtrl, "");
+
 // NT: rows of a tile.  PAIR: a tile of twice the weight rows by two CTAs (cta_group::2), each
 // with its own weight rows in its TMEM and half of the activation rows in its shared memory.
 template <int NT, bool PAIR>
 struct Shape {
-  static constexpr uint32_t accs = 256 / NT;                 // accumulators, NT columns each
-  static constexpr uint32_t a_column = 256;                  // first TMEM column of the weights
-  static constexpr uint32_t ring = 8;                        // stages of 64 along K
+  // stages of 64 along K: 32 TMEM columns of weights each; accumulators take the others
+  static constexpr uint32_t ring = NT == 32 ? 10 : 8;
+  static constexpr uint32_t a_column = 512 - ring * 32;      // first TMEM column of the weights
+  static constexpr uint32_t accs = a_column / NT < 8 ? a_column / NT : 8;
   static constexpr int rows = PAIR ? NT / 2 : NT;            // activation rows of a CTA
   static constexpr uint32_t x_bytes = rows * 128;            // ... and their bytes in a stage
   static constexpr int epi = NT >= 128 ? 8 : 4;              // epilogue warps
   static constexpr int w_sets = NT >= 128 ? 1 : 2;           // sets of weight converters
-  static constexpr int x_warps = rows / 32;                  // activation converters of a set
-  static constexpr int sets = NT >= 128 ? 2 : 4;                 // sets of them
+  static constexpr int x_warps = NT == 32 ? 2 : rows / 32;  // activation converters of a set
+  static constexpr int passes = rows / (x_warps * 4);        // rows of a converting lane
+  static constexpr int sets = NT >= 128 ? 2 : (int)ring / 2;                // sets of them
   static constexpr int epi0 = 2 + 4 * w_sets, x0 = epi0 + epi;  // first warps
   static constexpr int relay0 = x0 + sets * x_warps;          // a pair's relaying warps
   static constexpr int relays = PAIR ? 4 : 0;
@@ -199,7 +205,7 @@ struct StepRing {
 template <bool SWIGLU, int NT, bool PAIR>
 __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
     k_int8_tc(const Fp8Args a, const __grid_constant__ Fp8Maps maps, const uint32_t n_w,
-              const int split_below) {
+              const int split_below, const int tile_rows, const bool pairs) {
   pdl_trigger();
   using S = Shape<NT, PAIR>;
   extern __shared__ __align__(1024) uint8_t tsm_raw[];
@@ -211,16 +217,16 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
   uint8_t *ctrl = xsm + S::ring * S::x_bytes;
   uint64_t *w_full = (uint64_t *)ctrl;     // [kMaxStages] weight bytes of a stage landed
   uint64_t *w_empty = w_full + kMaxStages;  // [kMaxStages] ... read
-  uint64_t *full = w_empty + kMaxStages;   // [8] a step's operands written
-  uint64_t *empty = full + 8;              // [8] ... consumed
-  uint64_t *d_full = empty + 8;            // [8] accumulator written
+  uint64_t *full = w_empty + kMaxStages;   // [kRing] a step's operands written
+  uint64_t *empty = full + kRing;          // [kRing] ... consumed
+  uint64_t *d_full = empty + kRing;           // [8] accumulator written
   uint64_t *d_empty = d_full + 8;          // [8] ... read
   uint64_t *meet_bar = d_empty + 8;        // the epilogue's warps
   uint64_t *drain = meet_bar + 1;          // the MMAs of an aborted call
   uint32_t *tmem_holder = (uint32_t *)(drain + 1);
   volatile int *abort_flag = (volatile int *)(tmem_holder + 1);
   volatile int *last_part = (volatile int *)(tmem_holder + 2);
-  float *xsc = (float *)(ctrl + 512);      // [2][NT] row scales of a tile
+  float *xsc = (float *)(ctrl + kCtrl);    // [2][NT] row scales of a tile
   int *tiles_sm = (int *)(xsc + 2 * NT);
 
   if (tid == 32) {
@@ -230,11 +236,13 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       bar_init(&w_full[i], 1);
-      bar_init(&w_empty[i], 4 * S::w_sets);
+      bar_init(&w_empty[i], S::w_sets >= 2 ? 8 : 4);
     }
-    for (uint32_t i = 0; i < 8; ++i) {
+    for (uint32_t i = 0; i < kRing; ++i) {
       bar_init(&full[i], 4 + S::x_warps + (PAIR && !(blockIdx.x & 1)));
       bar_init(&empty[i], 1);
+    }
+    for (uint32_t i = 0; i < 8; ++i) {
       bar_init(&d_full[i], 1);
       bar_init(&d_empty[i], S::ctas * S::epi);
     }
@@ -263,7 +271,7 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
   const uint32_t tmem = *tmem_holder;
   fp8_warm(a);
   pdl_wait();
-  const RowTiles rt = fp8_row_tiles<NT>(a, tiles_sm);
+  const RowTiles rt = fp8_row_tiles<NT>(a, tiles_sm, tile_rows);
   const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;
   Walk walk(rt.total * (int)a.n_tiles, a, (int)blockIdx.x / S::ctas, (int)gridDim.x / S::ctas,
             split_below);
@@ -278,7 +286,7 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
     // ============================ weights
     Ring st;
     while (!guard.aborted() && walk.take(seg)) {
-      const Fp8Tile t = fp8_tile<NT>(a, rt, seg.tile);
+      const Fp8Tile t = fp8_tile<NT>(a, rt, seg.tile, tile_rows);
       for (int kb = seg.kb0; kb < seg.kb1; ++kb, st.next(n_w)) {
         bar_wait(&w_empty[st.i], st.phase ^ 1, guard);  // the first use passes
         __syncwarp();
@@ -307,7 +315,7 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
         for (int s = 0; s < steps; ++s) st.next(S::ring);
         continue;
       }
-      const Fp8Tile t = fp8_tile<NT>(a, rt, seg.tile);
+      const Fp8Tile t = fp8_tile<NT>(a, rt, seg.tile, tile_rows);
       // M = 128, or 256 of a pair
       const uint32_t idesc = idesc_for((uint32_t)mma_rows(t.rows)) + (PAIR ? 8u << 24 : 0u);
       const uint32_t d = tmem + acc.i * NT;
@@ -334,23 +342,29 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
     }
   } else if (warp < S::epi0) {
     // ============================ weight converters: half `set` of each stage
-    const int set = S::w_sets == 2 ? (warp - 2) >> 2 : 0, quarter = warp & 3;
+    const int set = (warp - 2) >> 2, quarter = warp & 3;
+    constexpr int kHalves = S::w_sets >= 2 ? 2 : 1;       // sets that share a block
+    constexpr int kTurns = S::w_sets / kHalves;           // blocks' sets take turns
     const int row = SWIGLU ? quarter * 16 + (lane & 15) + (lane >> 4) * 64 : quarter * 32 + lane;
     const uint32_t dst = tmem + S::a_column + ((uint32_t)(quarter * 32) << 16);
-    Ring ws;
-    StepRing<S::w_sets> st(set);
+    StepRing<kTurns> ws(set / kHalves);
+    StepRing<kTurns> st(set / kHalves);  // of pairs of steps
+    int first = set / kHalves;           // this set's first block of the segment
     while (!guard.aborted() && walk.take(seg)) {
-      for (int kb = seg.kb0; kb < seg.kb1; ++kb, ws.next(n_w)) {
+      for (int kb = seg.kb0 + first; kb < seg.kb1;
+           kb += kTurns, ws.next(n_w), st.next(S::ring / 2)) {
         bar_wait(&w_full[ws.i], ws.phase, guard);
         // 128-byte swizzle: chunk c of row r at c ^ (r % 8)
         const uint8_t *src = tsm + ws.i * kWBytes + row * 128;
 #pragma unroll
-        for (int h = set; h < 2; h += S::w_sets, st.next(S::ring)) {
+        for (int h0 = 0; h0 < 2; h0 += kHalves) {
+          const int h = kHalves == 2 ? set & 1 : h0;
+          const uint32_t stage = 2 * st.i + h;
           uint4 v[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             v[c] = *(const uint4 *)(src + (((h * 4 + c) ^ (row & 7)) << 4));
-          if (S::w_sets == 2 || h == 1) {
+          if (h0 + kHalves == 2) {
             __syncwarp();
             if (lane == 0) bar_arrive(&w_empty[ws.i]);
           }
@@ -362,16 +376,17 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
             i8x4_to_f16(v[c].z, r[8 * c + 4], r[8 * c + 5]);
             i8x4_to_f16(v[c].w, r[8 * c + 6], r[8 * c + 7]);
           }
-          bar_wait(&empty[st.i], st.phase ^ 1, guard);
+          bar_wait(&empty[stage], st.phase ^ 1, guard);
           tc_fence_after();
           __syncwarp();
-          tc_st32(dst + st.i * 32, r);
+          tc_st32(dst + stage * 32, r);
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) bar_arrive(&full[st.i]);
+          if (lane == 0) bar_arrive(&full[stage]);
         }
       }
+      first = (first - (seg.kb1 - seg.kb0) % kTurns + kTurns) % kTurns;
     }
   } else if (warp < S::x0) {
     // ============================ epilogue
@@ -385,7 +400,7 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
       __syncwarp();
     };
     while (!guard.aborted() && walk.take(seg)) {
-      const Fp8Tile t = fp8_tile<NT>(a, rt, seg.tile);
+      const Fp8Tile t = fp8_tile<NT>(a, rt, seg.tile, tile_rows);
       // ---- scales: one a row through shared memory, one a lane
       float *xs = xsc + (tiles++ & 1) * NT;
       for (int r = ew * 32 + lane; r < t.rows; r += S::epi * 32)
@@ -408,9 +423,18 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
           s[i + 2] = v[i + 2] * (x.z * ws);
           s[i + 3] = v[i + 3] * (x.w * ws);
         }
+        // SwiGLU: lanes of gate rows take row i0 + 2i, those of up rows the next
+        auto swiglu8 = [&](int i0, float (&h)[4]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = s[i0 + 2 * i], y = s[i0 + 2 * i + 1];
+            const float got = __shfl_xor_sync(0xffffffffu, up ? x : y, 16);
+            h[i] = fp8_swiglu_value(up ? got : x, up ? y : got);
+          }
+        };
+        // eight rows at a time without a branch between them: their latencies overlap
         auto store = [&](auto *p, auto from) {
           p += (size_t)(t.row0 + c) * a.ld + n;
-          // eight rows at a time without a branch between them: their latencies overlap
 #pragma unroll
           for (int i0 = 0; i0 < 32; i0 += 8) {
             if (i0 >= rows) break;  // the warp alike
@@ -420,13 +444,7 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
                 if (n < a.N && i < rows) p[(size_t)i * a.ld] = from(s[i]);
             } else {
               float h[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                // lanes of gate rows take row i0 + 2i, those of up rows the next
-                const float x = s[i0 + 2 * i], y = s[i0 + 2 * i + 1];
-                const float got = __shfl_xor_sync(0xffffffffu, up ? x : y, 16);
-                h[i] = fp8_swiglu_value(up ? got : x, up ? y : got);
-              }
+              swiglu8(i0, h);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int r = i0 + 2 * i + up;
@@ -435,7 +453,34 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
             }
           }
         };
+        // 16-bit types, two channels a store: a lane pair's even lane takes the first of two
+        // values, the odd lane the second
+        auto store2 = [&](auto pack) {
+          const bool odd = lane & 1;
+          uint16_t *p = (uint16_t *)a.out + (size_t)(t.row0 + c) * a.ld + (n & ~1u);
+          auto two = [&](float first, float second, int r0, int r1) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? first : second, 1);
+            const uint32_t w = odd ? pack(got, second) : pack(first, got);
+            const int r = odd ? r1 : r0;
+            if (n < a.N && r < rows) *(uint32_t *)(p + (size_t)r * a.ld) = w;
+          };
+#pragma unroll
+          for (int i0 = 0; i0 < 32; i0 += 8) {
+            if (i0 >= rows) break;  // the warp alike
+            if (!SWIGLU) {
+#pragma unroll
+              for (int i = i0; i < i0 + 8; i += 2) two(s[i], s[i + 1], i, i + 1);
+            } else {
+              float h[4];
+              swiglu8(i0, h);
+              two(h[0], h[1], i0 + up, i0 + 2 + up);
+              two(h[2], h[3], i0 + 4 + up, i0 + 6 + up);
+            }
+          }
+        };
         if (a.odt == MOE_DT_F32) store((float *)a.out, [](float x) { return x; });
+        else if (a.odt == MOE_DT_BF16 && pairs) store2(pack2<MOE_DT_BF16>);
+        else if (pairs) store2(pack2<MOE_DT_F16>);
         else if (a.odt == MOE_DT_BF16) store((__nv_bfloat16 *)a.out, Elem<MOE_DT_BF16>::from);
         else store((__half *)a.out, Elem<MOE_DT_F16>::from);
       };
@@ -531,12 +576,12 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
     const int xw = warp - S::x0, set = xw / S::x_warps;
     const int th = (xw - set * S::x_warps) * 32 + lane, chunk = th & 7, r0 = th >> 3;
     const int step = chunk >> 2, c0 = 2 * (chunk & 3);  // 16-byte chunks c0, c0 + 1 of fp16
-    constexpr int kPass = S::x_warps * 4, kPasses = 8;  // rows of a pass over the set's threads
+    constexpr int kPass = S::x_warps * 4, kPasses = S::passes;  // rows of a pass over the set's threads
     constexpr uint32_t kBlocks = S::ring / 2;
     StepRing<S::sets> st(set);
     int first = set;  // this set's first block of the segment
     while (!guard.aborted() && walk.take(seg)) {
-      const Fp8Tile t = fp8_tile<NT>(a, rt, seg.tile);
+      const Fp8Tile t = fp8_tile<NT>(a, rt, seg.tile, tile_rows);
       const int rows = mma_rows(t.rows) / S::ctas;  // this CTA's
       int row[kPasses];  // a bad one (flagged) reads row 0
 #pragma unroll
@@ -616,7 +661,7 @@ cudaError_t run_tc(Fp8Args &a, cudaStream_t stream) {
     if (!byte_map(&maps.w[m], a.wq[m], a.K, a.N, a.E, 3, channels)) return cudaErrorInvalidValue;
   auto kern = k_int8_tc<SWIGLU, NT, PAIR>;
   const size_t rest =
-      1024 + S::ring * (size_t)S::x_bytes + 512 + 4 * 2 * NT + fp8_tiles_smem(a.E);
+      1024 + S::ring * (size_t)S::x_bytes + kCtrl + 4 * 2 * NT + fp8_tiles_smem(a.E);
   int n_w = (int)((kSmemLimit - rest) / kWBytes);
   if (n_w > kMaxStages) n_w = kMaxStages;
   const size_t smem = rest + (size_t)n_w * kWBytes;
@@ -636,15 +681,40 @@ cudaError_t run_tc(Fp8Args &a, cudaStream_t stream) {
   attr[1].val.clusterDim = {2, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = PAIR ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, maps, (uint32_t)n_w, split_below);
+  const bool pairs = ((uintptr_t)a.out & 3) == 0 && a.ld % 2 == 0 && a.N % 2 == 0;
+  // One expert's rows (their number is known here) in tiles that fill the last round of
+  // workers best.  A tile costs its rows and about 24 more (4000 rows, 4096 channels: 18
+  // tiles of 224 rows in place of 16 of 256).
+  int tile_rows = NT;
+  if (PAIR && a.E == 1) {
+    uint64_t least = ~0ull;
+    for (int mt = NT; mt >= NT / 2; mt -= 32) {
+      const uint64_t tiles = (uint64_t)((a.R + mt - 1) / mt) * a.n_tiles;
+      const uint64_t cost = (tiles + sms / S::ctas - 1) / (sms / S::ctas) * (mt + 24);
+      if (cost < least) {
+        least = cost;
+        tile_rows = mt;
+      }
+    }
+  }
+  return cudaLaunchKernelEx(&cfg, kern, a, maps, (uint32_t)n_w, split_below, tile_rows, pairs);
 }
+
+// The call's rows an expert, on average, choose the tile.  32 experts, gate/up 4096 -> 2 x 2048
+// and down 2048 -> 4096, a router's spread of rows (us):
+//   rows            8        16        32        64        96       128       192       512
+//   tile  32    87  49   95  53   116  65   189 105   264 146   335 185   480 263  1208 659
+//         64    88  50   92  53   107  62   137  80   184 107   230 133   320 185   760 440
+//        128   106  57  109  58   115  63   143  78   168  92   194 105   270 145   594 316
+//   256 pair   145  78  146  79   150  83   157  90   171 100   187 113   217 133   427 256
+constexpr uint64_t kRows32 = 12;
 
 template <bool SWIGLU>
 cudaError_t run_by_rows(Fp8Args &a, cudaStream_t stream) {
   const uint64_t R = a.R, E = a.E;
-  if (R <= 24 * E) return run_tc<SWIGLU, 32, false>(a, stream);
-  if (R <= 64 * E) return run_tc<SWIGLU, 64, false>(a, stream);
-  if (R <= 128 * E) return run_tc<SWIGLU, 128, false>(a, stream);
+  if (R <= kRows32 * E) return run_tc<SWIGLU, 32, false>(a, stream);
+  if (R <= (SWIGLU ? 72 : 56) * E) return run_tc<SWIGLU, 64, false>(a, stream);
+  if (R <= (SWIGLU ? 104 : 144) * E) return run_tc<SWIGLU, 128, false>(a, stream);
   return run_tc<SWIGLU, 256, true>(a, stream);
 }
 
@@ -657,7 +727,7 @@ bool int8_tc_ok(const Fp8Args &a) {
 
 // two shares a CTA of the largest tile that a call of so many rows may split
 size_t int8_tc_ws(uint32_t rows) {
-  return (size_t)fp8_ctas() * 2 * (rows <= 24 ? 32 : 64) * 128 * 4;
+  return (size_t)fp8_ctas() * 2 * (rows <= kRows32 ? 32 : 64) * 128 * 4;
 }
 
 cudaError_t launch_int8_tc(Fp8Args &a, bool swiglu, cudaStream_t stream) {
