@@ -68,7 +68,7 @@ struct Shape {
   static constexpr int relays = PAIR ? 4 : 0;
   static constexpr int threads = (relay0 + relays) * 32;
   static constexpr int cols = NT / (epi / 4);                // columns of an epilogue warp
-  static constexpr bool split = !PAIR && NT <= 64;           // tiles may be shared along K
+  static constexpr bool split = NT == 32;                    // tiles may be shared along K
   static constexpr int ctas = PAIR ? 2 : 1;
   static_assert(sets <= (int)ring / 2 && cols % 32 == 0, "");
 };
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
 }
 
 template <bool SWIGLU, int NT, bool PAIR>
-cudaError_t run_tc(Fp8Args &a, cudaStream_t stream) {
+cudaError_t run_tc(Fp8Args &a, cudaStream_t stream, int tile_rows = NT) {
   using S = Shape<NT, PAIR>;
   const int sms = fp8_ctas() / S::ctas * S::ctas;
   if (sms < S::ctas) return cudaErrorInvalidValue;
@@ -668,7 +668,9 @@ cudaError_t run_tc(Fp8Args &a, cudaStream_t stream) {
   static std::atomic<bool> done[kMaxDevices];
   const cudaError_t e = allow_smem(kern, done);
   if (e != cudaSuccess) return e;
-  const int split_below = S::split && a.nbk >= 16 ? sms / 4 : 0;
+  // A last round of few tiles of a long K is shared along K: a meeting costs ~5 us (16 rows,
+  // 4096 channels, K 6144: 16.9 us, 20 whole; 64 rows, 2048 channels, K 2048: 13.0 and 10).
+  const int split_below = S::split && a.nbk >= 32 ? sms / 4 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = sms;
   cfg.blockDim = S::threads;
@@ -682,21 +684,6 @@ cudaError_t run_tc(Fp8Args &a, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = PAIR ? 2 : 1;
   const bool pairs = ((uintptr_t)a.out & 3) == 0 && a.ld % 2 == 0 && a.N % 2 == 0;
-  // One expert's rows (their number is known here) in tiles that fill the last round of
-  // workers best.  A tile costs its rows and about 24 more (4000 rows, 4096 channels: 18
-  // tiles of 224 rows in place of 16 of 256).
-  int tile_rows = NT;
-  if (PAIR && a.E == 1) {
-    uint64_t least = ~0ull;
-    for (int mt = NT; mt >= NT / 2; mt -= 32) {
-      const uint64_t tiles = (uint64_t)((a.R + mt - 1) / mt) * a.n_tiles;
-      const uint64_t cost = (tiles + sms / S::ctas - 1) / (sms / S::ctas) * (mt + 24);
-      if (cost < least) {
-        least = cost;
-        tile_rows = mt;
-      }
-    }
-  }
   return cudaLaunchKernelEx(&cfg, kern, a, maps, (uint32_t)n_w, split_below, tile_rows, pairs);
 }
 
@@ -709,9 +696,43 @@ cudaError_t run_tc(Fp8Args &a, cudaStream_t stream) {
 //   256 pair   145  78  146  79   150  83   157  90   171 100   187 113   217 133   427 256
 constexpr uint64_t kRows32 = 12;
 
+// One expert's rows are known here, so that whole rounds of tiles can be counted: a call's
+// time is about a fixed part and, for each round, so much a step of 64 along K (measured over
+// 64 to 8000 rows, 512 to 4096 channels, K 1024 to 6144; in 10 ns).  A pair's tiles are cut to
+// a height that fills its last round (4000 rows, 4096 channels: 18 of 224 rows).
+struct OneExpert {
+  int tile = 0, rows = 0;  // NT (256: pairs) and the rows of a tile
+  OneExpert(uint32_t R, uint32_t N, uint32_t K, bool swiglu, int sms) {
+    const uint64_t steps = (K + 63) / 64, channels = swiglu ? 64 : 128;
+    uint64_t least = ~0ull;
+    auto take = [&](int nt, int height, uint64_t columns, int workers, uint64_t fixed,
+                    uint64_t step) {
+      const uint64_t tiles = (uint64_t)((R + height - 1) / height) * ((N + columns - 1) / columns);
+      const uint64_t cost = fixed + (tiles + workers - 1) / workers * steps * step;
+      if (cost < least) {
+        least = cost;
+        tile = nt;
+        rows = height;
+      }
+    };
+    take(32, 32, channels, sms, 420, 18);
+    take(64, 64, channels, sms, 460, 20);
+    take(128, 128, channels, sms, 450, 30);
+    for (int h = 256; h >= 128 && sms > 1; h -= 32)
+      take(256, h, 2 * channels, sms / 2, 650, (uint64_t)(h + 24) / 8);
+  }
+};
+
 template <bool SWIGLU>
 cudaError_t run_by_rows(Fp8Args &a, cudaStream_t stream) {
   const uint64_t R = a.R, E = a.E;
+  if (E == 1) {
+    const OneExpert best(a.R, a.N, a.K, SWIGLU, fp8_ctas());
+    if (best.tile == 32) return run_tc<SWIGLU, 32, false>(a, stream);
+    if (best.tile == 64) return run_tc<SWIGLU, 64, false>(a, stream);
+    if (best.tile == 128) return run_tc<SWIGLU, 128, false>(a, stream);
+    return run_tc<SWIGLU, 256, true>(a, stream, best.rows);
+  }
   if (R <= kRows32 * E) return run_tc<SWIGLU, 32, false>(a, stream);
   if (R <= (SWIGLU ? 72 : 56) * E) return run_tc<SWIGLU, 64, false>(a, stream);
   if (R <= (SWIGLU ? 104 : 144) * E) return run_tc<SWIGLU, 128, false>(a, stream);
@@ -725,9 +746,10 @@ bool int8_tc_ok(const Fp8Args &a) {
   return a.K % 16 == 0 && a16(a.xq) && a16(a.wq[0]) && a16(a.wq[1]) && encode_fn() != nullptr;
 }
 
-// two shares a CTA of the largest tile that a call of so many rows may split
+// two shares a CTA of a tile of 32 rows
 size_t int8_tc_ws(uint32_t rows) {
-  return (size_t)fp8_ctas() * 2 * (rows <= kRows32 ? 32 : 64) * 128 * 4;
+  (void)rows;
+  return (size_t)fp8_ctas() * 2 * 32 * 128 * 4;
 }
 
 cudaError_t launch_int8_tc(Fp8Args &a, bool swiglu, cudaStream_t stream) {
