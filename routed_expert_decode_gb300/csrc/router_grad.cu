@@ -100,12 +100,12 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __
 __device__ __forceinline__ float2 exp_of_minus(float2 x) {
   constexpr float kHi = 1.4426950216293335f, kLo = 1.9259629911266175e-8f;  // log2 e
   constexpr float kLn2 = 0.6931471805599453f;
-  const float2 t = mul2(x, both(-0.5f * kHi));
+  const float2 t = mul2(x, both(0.5f * kHi));
   // half of what is missing from the exponent
-  const float2 rest = fma2(x, both(-0.5f * kLo), fma2(x, both(-0.5f * kHi), make_float2(-t.x, -t.y)));
+  const float2 rest = fma2(x, both(-0.5f * kLo), fma2(x, both(-0.5f * kHi), t));
   float2 e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(-t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(-t.y));
   e = fma2(mul2(e, both(kLn2)), rest, e);
   return mul2(e, e);
 }
@@ -203,9 +203,18 @@ __device__ __forceinline__ float scores(uint32_t fn, const Team &tm, float2 (&l)
 __device__ __forceinline__ int seq_at(const moe_tokens &t, uint32_t s) {
   return t.seq ? min(max(t.seq[s], 0), (int)t.T) : s == 0 ? 0 : (int)t.T;
 }
-// the first sequence that ends behind token x (S: none)
+// The first sequence that ends behind token x (S: none), by a whole warp: as many as end at
+// or before it, counted 32 at a time for few sequences.
 __device__ __forceinline__ uint32_t seq_of(const moe_tokens &t, int x) {
   uint32_t lo = 0, hi = t.S;
+  if (hi <= 128) {
+#pragma unroll
+    for (uint32_t i = 0; i < 128; i += 32) {
+      const uint32_t s = i + (threadIdx.x & 31);
+      if (i < hi) lo += __popc(__ballot_sync(kAll, s < hi && seq_at(t, min(s, hi - 1) + 1) <= x));
+    }
+    return lo;
+  }
   while (lo < hi) {
     const uint32_t mid = (lo + hi) / 2;
     if (seq_at(t, mid + 1) > x) hi = mid;
@@ -290,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 4 : 2) k_balance(const Bal
   const bool alone = gridDim.x == 1;
   const int t0 = (int)min(a.g.t.T, blockIdx.x * a.per);
   const int t1 = (int)min((uint64_t)a.g.t.T, (uint64_t)t0 + a.per);
-  constexpr int U = NC == 1 ? 4 : 2;  // tokens of a team on the way together
+  constexpr int U = NC == 1 ? 2 : 1;  // tokens of a team at a time, the next on their way
   const int step = kWarps * (int)tm.per_warp();
   for (uint32_t s = alone ? 0 : seq_of(a.g.t, t0); s < a.g.t.S; ++s) {
     const int s0 = seq_at(a.g.t, s), s1 = seq_at(a.g.t, s + 1);
@@ -314,15 +323,19 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 4 : 2) k_balance(const Bal
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[c][i] = both(0.0f);
-    for (int base = lo + warp * (int)tm.per_warp(); base < hi; base += U * step) {
-      Row<DT, NC> row[U];
-      bool on[U];
+    Row<DT, NC> row[U], next[U];
+    bool on[U], next_on[U];
+    auto fetch = [&](Row<DT, NC>(&r)[U], bool(&o)[U], int base) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int t = base + u * step + tm.t;
-        on[u] = t < hi && (!a.g.t.live || a.g.t.live[t]);
-        row[u].load(a.g.logits, a.g.ld, (uint32_t)t, E, tm, a.vec, on[u]);
+        o[u] = t < hi && (!a.g.t.live || a.g.t.live[t]);
+        r[u].load(a.g.logits, a.g.ld, (uint32_t)t, E, tm, a.vec, o[u]);
       }
+    };
+    fetch(row, on, lo + warp * (int)tm.per_warp());
+    for (int base = lo + warp * (int)tm.per_warp(); base < hi; base += U * step) {
+      fetch(next, next_on, base + U * step);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float2 l[NC][4];
@@ -333,6 +346,8 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 4 : 2) k_balance(const Bal
         for (int c = 0; c < NC; ++c)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[c][i] = fma2(l[c][i], both(inv), acc[c][i]);
+        row[u] = next[u];
+        on[u] = next_on[u];
       }
     }
     // ---- picks, a thread a token
@@ -543,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? kBackCtas : NC == 2 ? 2 : 
       a.count ? (a.dloss ? a.dloss[0] : 1.0f) *
                     __fdiv_rn(a.g.coef * (float)E, (float)a.g.t.S * (float)k)
               : 0.0f;
-  uint32_t s = a.count ? seq_of(a.g.t, (int)t) : 0;
+  uint32_t s = a.count ? seq_of(a.g.t, (int)(g0 * nt)) : 0;  // of the warp's first token
   int s_begin = 0, s_end = 0;
   uint32_t have = 0xffffffffu;  // the sequence whose coefficients coef holds
   float2 coef[NC][4];
