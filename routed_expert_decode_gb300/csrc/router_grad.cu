@@ -10,7 +10,7 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kBackCtas = 4;  // CTAs an SM of the logits' gradient (65536 x 256 bf16: 39 us, 43 with 3)
+constexpr int kBackCtas = 3;  // CTAs an SM of the logits' gradient (65536 x 256 bf16: 38 us, 40 with 4, 44 with 2)
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -119,10 +119,10 @@ __device__ __forceinline__ float2 rcp2(float2 x) {
 
 // l -> scores p (softmax: whose sum is 1), in place; slope = d log p / dl, softmax's
 // without its sum's part.  A NaN counts as -inf, +inf as the largest finite value.
-// Returns the sum of p.
+// Returns the sum of p; top and norm: softmax's maximum of l and the factor of e^(l - top).
 template <int NC, bool SLOPE, typename Team>
 __device__ __forceinline__ float scores(uint32_t fn, const Team &tm, float2 (&l)[NC][4],
-                                        float2 (&slope)[NC][4]) {
+                                        float2 (&slope)[NC][4], float &top, float &norm) {
   float2 s = both(0.0f);
   if (fn == MOE_SCORE_SOFTMAX) {
     float m = -FLT_MAX;  // of a row of -inf: every term is 0
@@ -147,6 +147,8 @@ __device__ __forceinline__ float scores(uint32_t fn, const Team &tm, float2 (&l)
       }
     const float sum = tm.sum(s.x + s.y);
     const float r = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+    top = m;
+    norm = r;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -197,6 +199,17 @@ __device__ __forceinline__ float scores(uint32_t fn, const Team &tm, float2 (&l)
       s = add2(s, v);
     }
   return tm.sum(s.x + s.y);
+}
+
+// p of one logit; softmax: e^(l - top), and 0 for -inf whatever top is
+__device__ __forceinline__ float score_of(uint32_t fn, float l, float top) {
+  if (fn == MOE_SCORE_SOFTMAX) return exp_of_minus(both(fminf(top - l, 110.0f))).x;
+  const float e = exp_of_minus(both(fminf(fabsf(l), 110.0f))).x;
+  if (fn == MOE_SCORE_SIGMOID) {
+    const float big = rcp2(both(1.0f + e)).x;
+    return l >= 0.0f ? big : e * big;
+  }
+  return __fsqrt_rn(fminf(fmaxf(l, 0.0f), FLT_MAX) + log1pf(e));
 }
 
 // ---------------------------------------------------------------- sequences
@@ -340,7 +353,8 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 4 : 2) k_balance(const Bal
       for (int u = 0; u < U; ++u) {
         float2 l[NC][4];
         row[u].to(l);
-        const float sum = scores<NC, false>(a.g.r.score, tm, l, l);
+        float top, norm;
+        const float sum = scores<NC, false>(a.g.r.score, tm, l, l, top, norm);
         const float inv = on[u] && sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -493,7 +507,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_balance_join(const BalanceArgs
 // ---------------------------------------------------------------- the logits' gradient
 struct RouteBackArgs {
   RouterGradArgs g;
-  uint32_t lanes, run;  // token groups of a warp
+  uint32_t lanes, run;  // of a team; tokens of a warp
+  uint32_t slots;       // lanes for a token's picks, a power of two
   bool vec, vec_out;
   const float *dw;
   const int32_t *count, *tokens;
@@ -522,43 +537,39 @@ __device__ __forceinline__ void store_row(const RouteBackArgs &a, uint32_t t, co
   }
 }
 
-// A warp takes `run` consecutive groups of tokens, the next one's logits and picks on the way
-// while it works on one; the loss's coefficients of a sequence's experts stay in registers
-// from token to token.  The picks' part goes through shared memory: p is laid out there for
-// the picks' lanes to fetch; they add theirs to a row of zeros, which every lane collects.
+// A warp takes `run` consecutive tokens, in batches.  First the picks of a whole batch, a lane a
+// slot (four tokens of up to 8 slots): their logits are read and scored by themselves, and
+// their part of the gradient goes to rows of zeros in shared memory.  Then the tokens, each
+// by its team, the next one's logits on their way: scores, the loss's part (whose
+// coefficients stay in registers from token to token), the picks' part from shared memory.
+// 65536 x 256 bf16, top 8, with the loss: 37.7 us (39.1 with the picks token by token, from p
+// laid out in shared memory), of which scores and stores alone are 20; bound by issue.
 template <int DT, int NC, bool WIDE>
 __global__ void __launch_bounds__(kThreads, NC == 1 ? kBackCtas : NC == 2 ? 2 : 1)
     k_route_backward(const RouteBackArgs a) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ __align__(16) uint8_t rsm[];
-  const uint32_t E = a.g.r.n_expert, k = a.g.r.top_k, fn = a.g.r.score;
+  const uint32_t E = a.g.r.n_expert, k = a.g.r.top_k, fn = a.g.r.score, T = a.g.t.T;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Team<WIDE> tm(a.lanes);
-  constexpr uint32_t kRounds = WIDE ? 1 : 8;
   const uint32_t width = NC * tm.lanes() * 8, nt = tm.per_warp();
-  float *pbuf = (float *)rsm + ((size_t)warp * nt + tm.t) * 2 * width;  // the team's scores
-  float *vbuf = pbuf + width;                                          // ... and zeros
-  const uint64_t g0 = ((uint64_t)blockIdx.x * kWarps + warp) * a.run;
-  const uint64_t groups = ((uint64_t)a.g.t.T + nt - 1) / nt;
-  if (g0 >= groups) return;
-  const uint32_t n_groups = (uint32_t)min((uint64_t)a.run, groups - g0);
-  uint32_t t = (uint32_t)(g0 * nt) + tm.t;
+  const uint32_t slots = a.slots, nb = 32 / slots;     // lanes of a token's picks, tokens
+  const uint32_t batch = nb > nt ? nb : nt;            // tokens of a batch
+  float *vbuf = (float *)rsm + (size_t)warp * batch * (width + 4);  // [batch][width] zeros
+  float *stat = vbuf + batch * width;                   // [batch][4] top and sum of the picks
+  const uint64_t first = ((uint64_t)blockIdx.x * kWarps + warp) * a.run;
+  if (first >= T) return;
+  const uint32_t t0 = (uint32_t)first, t1 = (uint32_t)min((uint64_t)T, first + a.run);
   const bool softmax = fn == MOE_SCORE_SOFTMAX;
-  auto put = [&](float *buf, const float2 (&v)[NC][4]) {
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      float4 *b = (float4 *)(buf + tm.expert(c));
-      b[0] = make_float4(v[c][0].x, v[c][0].y, v[c][1].x, v[c][1].y);
-      b[1] = make_float4(v[c][2].x, v[c][2].y, v[c][3].x, v[c][3].y);
-    }
-  };
+  for (uint32_t i = lane * 4; i < batch * (width + 4); i += 128)
+    *(float4 *)(vbuf + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   // factor of a sequence's loss gradient, up to 1 / n^2
   const float factor =
       a.count ? (a.dloss ? a.dloss[0] : 1.0f) *
                     __fdiv_rn(a.g.coef * (float)E, (float)a.g.t.S * (float)k)
               : 0.0f;
-  uint32_t s = a.count ? seq_of(a.g.t, (int)(g0 * nt)) : 0;  // of the warp's first token
+  uint32_t s = a.count ? seq_of(a.g.t, (int)t0) : 0;
   int s_begin = 0, s_end = 0;
   uint32_t have = 0xffffffffu;  // the sequence whose coefficients coef holds
   float2 coef[NC][4];
@@ -566,145 +577,179 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? kBackCtas : NC == 2 ? 2 : 
   for (int c = 0; c < NC; ++c)
 #pragma unroll
     for (int j = 0; j < 4; ++j) coef[c][j] = both(0.0f);
-  if (a.dw) put(vbuf, coef);
   if (a.count && s < a.g.t.S) {
     s_begin = seq_at(a.g.t, s);
     s_end = seq_at(a.g.t, s + 1);
   }
-  // slots of this lane: l, l + lanes, ...
-  const uint32_t rounds = WIDE ? 1 : (k + tm.lanes() - 1) / tm.lanes();  // 8 at most: k <= E
+  // ---- this lane's slot of a batch: pick (E: none) and dw two batches ahead, its logit one
+  const uint32_t slot = (uint32_t)lane & (slots - 1), of = (uint32_t)lane / slots;
+  auto pick_at = [&](uint32_t x, uint32_t &e, float &g) {
+    const bool in = a.dw && slot < k && x < t1;
+    e = in ? min((uint32_t)a.g.idx[(size_t)x * k + slot], E) : E;
+    g = e < E ? a.dw[(size_t)x * k + slot] : 0.0f;
+  };
+  auto logit_at = [&](uint32_t x, uint32_t e) {
+    using X = Elem<DT>;
+    return e < E ? logit_value(X::to(((const typename X::T *)a.g.logits)[(size_t)x * a.g.ld + e]))
+                 : -INFINITY;
+  };
+  auto group_sum = [&](float v) {
+    for (uint32_t o = slots >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+  };
+  // one lane's slot: its part of the gradient to row r
+  auto picks = [&](uint32_t r, uint32_t e, float g, float l) {
+    float top = 0.0f;
+    if (softmax) {  // of the picks: the row's is not known yet
+      top = e < E ? l : -FLT_MAX;
+      for (uint32_t o = slots >> 1; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+      top = fmaxf(top, -FLT_MAX);
+    }
+    const float p = e < E ? score_of(fn, l, top) : 0.0f;
+    const float dots = group_sum(p * g);
+    float v = a.g.r.s * p * g;
+    if (a.g.r.renorm) {
+      const float total = group_sum(p);
+      const float inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
+      v = a.g.r.s * (p * inv) * (g - dots * inv);
+    }
+    if (softmax && slot == 0) {
+      stat[4 * r] = top;
+      stat[4 * r + 1] = dots;
+    }
+    // the lanes one after another where two of them have the same expert
+    const uint32_t key = e < E ? r * 1024 + e : 0x80000000u + (uint32_t)lane;
+    const uint32_t same = __match_any_sync(kAll, key);
+    const uint32_t before = __popc(same & ((1u << lane) - 1u));
+    for (uint32_t turn = 0; __any_sync(kAll, before >= turn); ++turn) {
+      if (before == turn && e < E) vbuf[r * width + e] += v;
+      __syncwarp();
+    }
+  };
+  uint32_t e1, e2;
+  float g1, g2, l1;
+  pick_at(t0 + of, e1, g1);
+  l1 = logit_at(t0 + of, e1);
+  pick_at(t0 + batch + of, e2, g2);
   Row<DT, NC> next;
-  uint32_t next_e = E;  // the first slot's pick and gradient
-  float next_g = 0.0f;
   bool next_live = true;
   auto fetch = [&](uint32_t x) {
-    const bool in = x < a.g.t.T;
-    next.load(a.g.logits, a.g.ld, x, E, tm, a.vec, in);
-    if (a.dw) {
-      const bool mine = in && (uint32_t)tm.l < k;
-      next_e = mine ? min((uint32_t)a.g.idx[(size_t)x * k + tm.l], E) : E;
-      next_g = mine ? a.dw[(size_t)x * k + tm.l] : 0.0f;
-    }
-    if (a.count && a.g.t.live) next_live = in && a.g.t.live[x];
+    next.load(a.g.logits, a.g.ld, x, E, tm, a.vec, x < t1);
+    if (a.count && a.g.t.live) next_live = x < t1 && a.g.t.live[x];
   };
-  fetch(t);
-  for (uint32_t i = 0; i < n_groups; ++i, t += nt) {
-    const bool on = t < a.g.t.T, live = next_live;
-    const uint32_t e0 = next_e;
-    const float w0 = next_g;
-    float2 p[NC][4], slope[NC][4], d[NC][4];
-    next.to(p);
-    if (i + 1 < n_groups) fetch(t + nt);
-    const float sum = scores<NC, true>(fn, tm, p, slope);
-    // ---- the loss's part
-    bool counts = false;
-    if (a.count && on) {
-      while (s < a.g.t.S && s_end <= (int)t) {
-        ++s;
-        if (s < a.g.t.S) {
-          s_begin = seq_at(a.g.t, s);
-          s_end = seq_at(a.g.t, s + 1);
-        }
-      }
-      counts = s < a.g.t.S && s_begin <= (int)t && live;
-      if (counts && s != have) {
-        const int32_t *cs = a.count + (size_t)s * E;
-        const float n = (float)max(a.tokens[s], 1), f = __fdiv_rn(factor, n * n);
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t e = tm.expert(c) + 2 * j;
-            coef[c][j] = make_float2(e < E ? f * (float)cs[e] : 0.0f,
-                                     e + 1 < E ? f * (float)cs[e + 1] : 0.0f);
-          }
-        have = s;
-      }
-    }
-    if (__any_sync(kAll, counts)) {
-      const float inv = counts && sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-      float2 dots = both(0.0f);
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dots = fma2(coef[c][j], p[c][j], dots);
-      const float dot = tm.sum(dots.x + dots.y) * inv;
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          d[c][j] = mul2(mul2(p[c][j], both(inv)), add2(coef[c][j], both(-dot)));
-    } else {
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) d[c][j] = both(0.0f);
-    }
-    // ---- the picks' part
+  fetch(t0 + tm.t);
+  __syncwarp();
+  for (uint32_t b0 = t0; b0 < t1; b0 += batch) {
     if (a.dw) {
-      put(pbuf, p);
-      __syncwarp();
-      float pk[kRounds], gk[kRounds];  // of this lane's slots: p and dw, 0 where there is none
-      uint32_t ek[kRounds];
-      float total = 0.0f, dots = 0.0f;
-#pragma unroll
-      for (uint32_t m = 0; m < kRounds; ++m) {
-        if (m >= rounds) break;
-        const uint32_t j = tm.l + m * tm.lanes();
-        ek[m] = m == 0 ? e0 : on && j < k ? min((uint32_t)a.g.idx[(size_t)t * k + j], E) : E;
-        gk[m] = m == 0 ? w0 : ek[m] < E ? a.dw[(size_t)t * k + j] : 0.0f;
-        pk[m] = ek[m] < E ? pbuf[ek[m]] : 0.0f;
-        total += pk[m];
-        dots = __fmaf_rn(pk[m], ek[m] < E ? gk[m] : 0.0f, dots);
+      picks(of, e1, g1, l1);
+      for (uint32_t sub = nb; sub < batch; sub += nb) {  // teams of more tokens than that
+        uint32_t e;
+        float g;
+        pick_at(b0 + sub + of, e, g);
+        picks(sub + of, e, g, logit_at(b0 + sub + of, e));
       }
-      total = tm.sum(total);
-      dots = tm.sum(dots);
-      const float inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
-      if (!a.g.r.renorm && softmax) {  // every expert's p falls as a pick's rises
+    }
+    const uint32_t e0 = e1;
+    e1 = e2;
+    g1 = g2;
+    l1 = logit_at(b0 + batch + of, e1);
+    pick_at(b0 + 2 * batch + of, e2, g2);
+    for (uint32_t i = 0; i < batch && b0 + i < t1; i += nt) {
+      const uint32_t t = b0 + i + tm.t;
+      const bool on = t < t1, live = next_live;
+      float2 p[NC][4], slope[NC][4], d[NC][4];
+      next.to(p);
+      if (b0 + i + nt < t1) fetch(t + nt);
+      float top = 0.0f, norm = 0.0f;
+      const float sum = scores<NC, true>(fn, tm, p, slope, top, norm);
+      // ---- the loss's part
+      bool counts = false;
+      if (a.count && on) {
+        while (s < a.g.t.S && s_end <= (int)t) {
+          ++s;
+          if (s < a.g.t.S) {
+            s_begin = seq_at(a.g.t, s);
+            s_end = seq_at(a.g.t, s + 1);
+          }
+        }
+        counts = s < a.g.t.S && s_begin <= (int)t && live;
+        if (counts && s != have) {
+          const int32_t *cs = a.count + (size_t)s * E;
+          const float n = (float)max(a.tokens[s], 1), f = __fdiv_rn(factor, n * n);
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t e = tm.expert(c) + 2 * j;
+              coef[c][j] = make_float2(e < E ? f * (float)cs[e] : 0.0f,
+                                       e + 1 < E ? f * (float)cs[e + 1] : 0.0f);
+            }
+          have = s;
+        }
+      }
+      if (__any_sync(kAll, counts)) {
+        const float inv = counts && sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+        float2 dots = both(0.0f);
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) d[c][j] = fma2(both(-a.g.r.s * dots), p[c][j], d[c][j]);
-      }
+          for (int j = 0; j < 4; ++j) dots = fma2(coef[c][j], p[c][j], dots);
+        const float dot = tm.sum(dots.x + dots.y) * inv;
 #pragma unroll
-      for (uint32_t m = 0; m < kRounds; ++m) {
-        if (m >= rounds) break;
-        const uint32_t e = ek[m];
-        const float v = a.g.r.renorm ? a.g.r.s * (pk[m] * inv) * (gk[m] - dots * inv)
-                                     : a.g.r.s * pk[m] * gk[m];
-        // the lanes one after another where two of them have the same expert
-        const uint32_t key = e < E ? (uint32_t)tm.t * 1024 + e : 0x80000000u + (uint32_t)lane;
-        const uint32_t same = __match_any_sync(kAll, key);
-        const uint32_t before = __popc(same & ((1u << lane) - 1u));
-        for (uint32_t turn = 0; __any_sync(kAll, before >= turn); ++turn) {
-          if (before == turn && e < E) vbuf[e] += v;
-          __syncwarp();
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            d[c][j] = mul2(mul2(p[c][j], both(inv)), add2(coef[c][j], both(-dot)));
+      } else {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d[c][j] = both(0.0f);
+      }
+      // ---- the picks' part
+      if (a.dw) {
+        const uint32_t r = i + tm.t;
+        float f = 1.0f;
+        if (softmax) {  // beside the row's largest logit; picks whose p is 0 weigh nothing
+          f = exp_of_minus(both(fminf(fmaxf(top - stat[4 * r], 0.0f), 110.0f))).x * norm;
+          if (a.g.r.renorm) f = f > 0.0f ? 1.0f : 0.0f;
+        }
+        if (softmax && !a.g.r.renorm) {  // every expert's p falls as a pick's rises
+          const float fall = -a.g.r.s * (stat[4 * r + 1] * f);
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[c][j] = fma2(both(fall), p[c][j], d[c][j]);
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const float4 *b = (const float4 *)(vbuf + r * width + tm.expert(c));
+          const float4 x = b[0], y = b[1];
+          d[c][0] = fma2(both(f), make_float2(x.x, x.y), d[c][0]);
+          d[c][1] = fma2(both(f), make_float2(x.z, x.w), d[c][1]);
+          d[c][2] = fma2(both(f), make_float2(y.x, y.y), d[c][2]);
+          d[c][3] = fma2(both(f), make_float2(y.z, y.w), d[c][3]);
         }
       }
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const float4 *b = (const float4 *)(vbuf + tm.expert(c));
-        const float4 x = b[0], y = b[1];
-        d[c][0] = add2(d[c][0], make_float2(x.x, x.y));
-        d[c][1] = add2(d[c][1], make_float2(x.z, x.w));
-        d[c][2] = add2(d[c][2], make_float2(y.x, y.y));
-        d[c][3] = add2(d[c][3], make_float2(y.z, y.w));
-      }
-      __syncwarp();
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (uint32_t m = 0; m < kRounds; ++m) {
-        if (m >= rounds) break;
-        if (ek[m] < E) vbuf[ek[m]] = 0.0f;
-      }
+        for (int j = 0; j < 4; ++j) d[c][j] = mul2(d[c][j], slope[c][j]);
+      if (!on) continue;
+      if (a.odt == MOE_DT_F32) store_row<MOE_DT_F32, NC>(a, t, tm, d);
+      else if (a.odt == MOE_DT_BF16) store_row<MOE_DT_BF16, NC>(a, t, tm, d);
+      else store_row<MOE_DT_F16, NC>(a, t, tm, d);
     }
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) d[c][j] = mul2(d[c][j], slope[c][j]);
-    if (!on) continue;
-    if (a.odt == MOE_DT_F32) store_row<MOE_DT_F32, NC>(a, t, tm, d);
-    else if (a.odt == MOE_DT_BF16) store_row<MOE_DT_BF16, NC>(a, t, tm, d);
-    else store_row<MOE_DT_F16, NC>(a, t, tm, d);
+    if (!a.dw) continue;
+    __syncwarp();
+    if (batch == nb) {
+      if (e0 < E) vbuf[of * width + e0] = 0.0f;
+    } else {
+      for (uint32_t i = lane * 4; i < batch * width; i += 128)
+        *(float4 *)(vbuf + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    __syncwarp();
   }
 }
 
@@ -806,14 +851,17 @@ cudaError_t balance_t(const BalanceArgs &a, unsigned grid, cudaStream_t stream) 
 template <int DT>
 cudaError_t route_backward_t(const RouteBackArgs &a, unsigned grid, cudaStream_t stream) {
   const int nc = chunks_of(a.g.r.n_expert);
-  const size_t smem = (size_t)kWarps * 32 * nc * 8 * 4 * 2;
-  if (a.lanes < 32) return launch_k(k_route_backward<DT, 1, false>, grid, kThreads, smem, stream, true, a);
-  if (nc == 1) return launch_k(k_route_backward<DT, 1, true>, grid, kThreads, smem, stream, true, a);
-  if (nc == 2) return launch_k(k_route_backward<DT, 2, true>, grid, kThreads, smem, stream, true, a);
-  static std::atomic<bool> done[kMaxDevices];
-  const cudaError_t e = allow_smem(k_route_backward<DT, 4, true>, done);
-  if (e != cudaSuccess) return e;
-  return launch_k(k_route_backward<DT, 4, true>, grid, kThreads, smem, stream, true, a);
+  const uint32_t width = nc * a.lanes * 8, nt = 32 / a.lanes, nb = 32 / a.slots;
+  const size_t smem = (size_t)kWarps * (nb > nt ? nb : nt) * (width + 4) * 4;
+  auto run = [&](auto kern, std::atomic<bool> *done) {
+    const cudaError_t e = allow_smem(kern, done);
+    return e != cudaSuccess ? e : launch_k(kern, grid, kThreads, smem, stream, true, a);
+  };
+  static std::atomic<bool> done[4][kMaxDevices];
+  if (a.lanes < 32) return run(k_route_backward<DT, 1, false>, done[0]);
+  if (nc == 1) return run(k_route_backward<DT, 1, true>, done[1]);
+  if (nc == 2) return run(k_route_backward<DT, 2, true>, done[2]);
+  return run(k_route_backward<DT, 4, true>, done[3]);
 }
 
 template <int DT, int YT>
@@ -888,10 +936,15 @@ cudaError_t launch_route_backward(const RouterGradArgs &g, const float *dw, cons
   a.dlogits = dlogits;
   a.odt = odt;
   a.ldd = ldd;
-  const uint64_t groups = ((uint64_t)g.t.T + 32 / a.lanes - 1) / (32 / a.lanes);
+  a.slots = 8;  // four tokens a batch: its rows of zeros are that many
+  while (a.slots < g.r.top_k) a.slots *= 2;
+  // as many warps as run at a time, whole batches each
+  const uint32_t nt = 32 / a.lanes, nb = 32 / a.slots, batch = nb > nt ? nb : nt;
+  const uint64_t batches = ((uint64_t)g.t.T + batch - 1) / batch;
   const uint64_t warps = (uint64_t)fp8_ctas() * kBackCtas * kWarps;
-  a.run = (uint32_t)((groups + warps - 1) / warps);
-  const unsigned grid = (unsigned)((groups + (uint64_t)a.run * kWarps - 1) / ((uint64_t)a.run * kWarps));
+  a.run = (uint32_t)((batches + warps - 1) / warps) * batch;
+  const unsigned grid =
+      (unsigned)(((uint64_t)g.t.T + (uint64_t)a.run * kWarps - 1) / ((uint64_t)a.run * kWarps));
   if (g.dt == MOE_DT_F32) return route_backward_t<MOE_DT_F32>(a, grid, stream);
   if (g.dt == MOE_DT_BF16) return route_backward_t<MOE_DT_BF16>(a, grid, stream);
   return route_backward_t<MOE_DT_F16>(a, grid, stream);
