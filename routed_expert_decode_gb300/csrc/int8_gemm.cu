@@ -113,7 +113,8 @@ cudaError_t run_core(Fp8Args &a, cudaStream_t stream) {
 // expert, K 6144: 4 rows 11.2 and 14.1, 8 rows (gate/up) 12 and 15, 12 rows 19 and 16; K 1024,
 // 8 rows: 12 and 7.
 bool few_rows(const Fp8Args &a) {
-  return 2ull * a.R <= (a.E > 8 ? a.E : 8) && (uint64_t)a.n_x * a.K <= 200 * 1024;
+  return 2ull * a.R <= (a.E > 8 ? a.E : 8) && (uint64_t)a.n_x * a.K <= 200 * 1024 &&
+         (uint64_t)a.R * (a.N / 2 + 1) < (1ull << 31);  // its units are numbered in 31 bits
 }
 
 }  // namespace

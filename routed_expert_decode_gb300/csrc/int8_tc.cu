@@ -694,7 +694,6 @@ cudaError_t run_tc(Fp8Args &a, cudaStream_t stream, int tile_rows = NT) {
 //         64    88  50   92  53   107  62   137  80   184 107   230 133   320 185   760 440
 //        128   106  57  109  58   115  63   143  78   168  92   194 105   270 145   594 316
 //   256 pair   145  78  146  79   150  83   157  90   171 100   187 113   217 133   427 256
-constexpr uint64_t kRows32 = 12;
 
 // One expert's rows are known here, so that whole rounds of tiles can be counted: a call's
 // time is about a fixed part and, for each round, so much a step of 64 along K (measured over
@@ -733,7 +732,7 @@ cudaError_t run_by_rows(Fp8Args &a, cudaStream_t stream) {
     if (best.tile == 128) return run_tc<SWIGLU, 128, false>(a, stream);
     return run_tc<SWIGLU, 256, true>(a, stream, best.rows);
   }
-  if (R <= kRows32 * E) return run_tc<SWIGLU, 32, false>(a, stream);
+  if (R <= (SWIGLU ? 12 : 20) * E) return run_tc<SWIGLU, 32, false>(a, stream);
   if (R <= (SWIGLU ? 72 : 56) * E) return run_tc<SWIGLU, 64, false>(a, stream);
   if (R <= (SWIGLU ? 104 : 144) * E) return run_tc<SWIGLU, 128, false>(a, stream);
   return run_tc<SWIGLU, 256, true>(a, stream);

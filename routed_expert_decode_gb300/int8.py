@@ -160,6 +160,11 @@ class Layer(fp8.Layer):
     The weights are this module's ``Mat``; h is held in x's type between its product and its
     quantiser."""
 
+    def __init__(self, router, gate, up, down, shared=None, keep_bytes: int = 4 << 30):
+        if not all(isinstance(m, Mat) for m in (gate, up, down, *(shared or ()))):
+            raise ValueError("the weights must be int8.Mat")
+        super().__init__(router, gate, up, down, shared, keep_bytes)
+
     def _make(self, T: int, dtype: torch.dtype) -> dict:
         E, k, d, f, R = self.E, self.router.top_k, self.d, self.f, T * self.router.top_k
         make = self._empty

@@ -351,3 +351,51 @@ def test_stream_and_graph(rg):
         logits.copy_(x.logits)
         graph.replay()
         check(x)
+
+
+def test_beyond_32_bit_offsets(rg):
+    """Logits of 8 GiB and expert rows of 12 GiB: the last tokens' results."""
+    T, E, k = (1 << 22) + 3, 1024, 2
+    g = torch.Generator(device="cuda").manual_seed(1)
+    logits = torch.zeros((T, E), dtype=torch.bfloat16, device="cuda")
+    tail = 40
+    logits[-tail:] = torch.randn((tail, E), generator=g, device="cuda").bfloat16()
+    idx = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    dw = torch.randn((T, k), generator=g, device="cuda")
+    r = router(E, k, 0)
+    out = torch.empty_like(logits)
+    rg.route_backward(r, logits, idx, out, dw=dw)
+    l, i, w = (t[-tail:].cpu().numpy() for t in (logits.float(), idx, dw))
+    want, bound = ref.route_backward(l, i, k, 0, True, 2.5, w)
+    bar = bound + (np.abs(want) + bound) * HALF_ULP["bf16"] + TINY["bf16"]
+    assert (np.abs(out[-tail:].double().cpu().numpy() - want) <= bar).all()
+    # counts of all of them, and a second sequence of the last
+    seq = torch.tensor([0, T - tail, T], dtype=torch.int32, device="cuda")
+    counts, tokens = torch.empty((2, E), dtype=torch.int32, device="cuda"), torch.empty(
+        2, dtype=torch.int32, device="cuda")
+    prob, loss = torch.empty((2, E), device="cuda"), torch.empty(1, device="cuda")
+    ws = torch.zeros(rg.workspace_size(r, T, 2), dtype=torch.uint8, device="cuda")
+    rg.balance(r, logits, idx, counts, tokens, prob, loss, ws, seq)
+    n = torch.bincount(idx[:-tail].flatten().long(), minlength=E)
+    assert torch.equal(counts[0].long(), n) and tokens.tolist() == [T - tail, tail]
+    rc, _, rp, _, e_prob, _ = ref.balance(l, i, k, 0)
+    assert np.array_equal(counts[1:].cpu().numpy(), rc)
+    assert (np.abs(prob[1:].cpu().numpy() - rp) <= rp * e_prob).all()
+    # equal logits: every share 1/E, each rounded as the bound of one says, summed over the
+    # tokens of a CTA's warp (900 in a row) and over CTAs
+    assert (prob[0] - 1.0 / E).abs().max().item() <= (70 + 900 + 700) * 2.0 ** -24 / E
+    del logits, out
+    R, d = (1 << 20) + 8, 6144
+    o = torch.zeros((R, d), dtype=torch.bfloat16, device="cuda")
+    o[-16:] = torch.randn((16, d), generator=g, device="cuda").bfloat16()
+    dy = torch.randn((2, d), generator=g, device="cuda").bfloat16()
+    pos = torch.arange(R - 16, R, dtype=torch.int32, device="cuda").view(2, 8)
+    w = torch.rand((2, 8), generator=g, device="cuda")
+    gw, go = torch.empty((2, 8), device="cuda"), torch.zeros_like(o)
+    rg.combine_backward(dy, o, w, pos, gw, go)
+    rw, ew, ro, eo = ref.combine_backward(dy.float().cpu().numpy(), o[-16:].float().cpu().numpy(),
+                                          w.cpu().numpy(), pos.cpu().numpy() - (R - 16))
+    assert (np.abs(gw.cpu().numpy() - rw) <= ew).all()
+    bar = eo + (np.abs(ro) + eo) * HALF_ULP["bf16"]
+    assert (np.abs(go[-16:].double().cpu().numpy() - ro) <= bar).all()
+    assert not go[:-16].any()
