@@ -38,14 +38,15 @@ def make_layer(g: torch.Generator) -> int8.Layer:
 
 
 def step(layer, w_router, x, target, seq, coef=0.01, rate=0.2):
-    """One step in place; returns (squared error, balance loss, the router's gradient)."""
+    """One step in place; returns (squared error a token, balance loss, the router's gradient).
+    The step's length is ``rate`` of the weights', against the gradient's direction."""
     logits = x.float() @ w_router.t()
     out = layer.forward(x, logits)
     diff = out.y.float() - target
-    grads = layer.router_gradients(out, logits, 2.0 * diff / diff.numel(), coef=coef, seq=seq)
+    grads = layer.router_gradients(out, logits, 2.0 * diff / len(diff), coef=coef, seq=seq)
     dw_router = grads.dlogits.t() @ x.float()
-    w_router.sub_(rate * dw_router)
-    return diff.square().mean(), grads.loss[0], dw_router
+    w_router.sub_(rate * w_router.norm() / dw_router.norm() * dw_router)
+    return diff.square().sum(1).mean(), grads.loss[0], dw_router
 
 
 def main() -> None:
@@ -62,7 +63,7 @@ def main() -> None:
         target = layer.forward(x, x.float() @ teacher.t()).y.float()
         err, loss, _ = step(layer, w_router, x, target, seq)
         if i % 10 == 0 or i == a.steps - 1:
-            print(f"step {i}: squared error {err:.4f}, balance loss {loss:.4f}")
+            print(f"step {i}: squared error {err:.1f}, balance loss {loss:.4f}")
 
 
 if __name__ == "__main__":
