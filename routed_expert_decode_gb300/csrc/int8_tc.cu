@@ -19,8 +19,8 @@
 // with its own 128 in its TMEM and half of the activation rows in its shared memory.  One
 // CTA's N side alone, fp16 written and read again, is all that its shared memory can move
 // while the tensor cores work (128 bytes a clock), and the fetches come on top: 16384 rows
-// of gate/up (d 6144, f 2048, 16 experts) take 770 us so, 532 in pairs (1.55 PFLOP/s; 470
-// without the conversions).  The first CTA issues; what it has to know of the second
+// of gate/up (d 6144, f 2048, 16 experts) take 770 us so, 525 in pairs (1.57 PFLOP/s; 470
+// without the activations' conversion, 480 without the epilogue).  The first CTA issues; what it has to know of the second
 // one's warps goes over four relaying warps there, because an arrival that makes the work
 // behind it visible to the other CTA takes ~800 clocks: with one warp for it 976 us, with the
 // converting warps making theirs 1390.
@@ -60,9 +60,9 @@ struct Shape {
   static constexpr uint32_t x_bytes = rows * 128;            // ... and their bytes in a stage
   static constexpr int epi = NT >= 128 ? 8 : 4;              // epilogue warps
   static constexpr int w_sets = NT >= 128 ? 1 : 2;           // sets of weight converters
-  static constexpr int x_warps = NT == 32 ? 2 : rows / 32;  // activation converters of a set
+  static constexpr int x_warps = NT == 32 ? 2 : rows / 32;   // activation converters of a set
   static constexpr int passes = rows / (x_warps * 4);        // rows of a converting lane
-  static constexpr int sets = NT >= 128 ? 2 : (int)ring / 2;                // sets of them
+  static constexpr int sets = NT >= 128 ? 2 : (int)ring / 2;  // sets of them
   static constexpr int epi0 = 2 + 4 * w_sets, x0 = epi0 + epi;  // first warps
   static constexpr int relay0 = x0 + sets * x_warps;          // a pair's relaying warps
   static constexpr int relays = PAIR ? 4 : 0;
