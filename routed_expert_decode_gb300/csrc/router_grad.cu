@@ -236,6 +236,17 @@ __device__ __forceinline__ uint32_t seq_of(const moe_tokens &t, int x) {
   return lo;
 }
 
+// the first sequence from s on that ends behind token x (S: none), by a thread for itself
+__device__ __forceinline__ uint32_t seq_from(const moe_tokens &t, uint32_t s, int x) {
+  uint32_t lo = s, hi = t.S;
+  while (lo < hi) {
+    const uint32_t mid = (lo + hi) / 2;
+    if (seq_at(t, mid + 1) > x) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
 // ---------------------------------------------------------------- the loss
 // CTA c has tokens [c*per, (c+1)*per), whatever sequences they are of.  What it
 // adds up of a sequence that lies within them it finishes itself; of one that goes on
@@ -245,6 +256,7 @@ __device__ __forceinline__ uint32_t seq_of(const moe_tokens &t, int x) {
 constexpr uint32_t kSumCtas = 4;      // an SM, at most (65536 x 256 bf16: 30 us; 34 with 6, 31 with 3)
 constexpr uint32_t kSumPasses = 4;  // tokens of a team, at least
 constexpr uint32_t kJoinRun = 32;   // experts of a joining CTA
+constexpr uint32_t kAloneSeqs = 4;  // sequences of a call that one CTA finishes, at most
 
 struct BalanceArgs {
   RouterGradArgs g;
@@ -309,16 +321,20 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 4 : 2) k_balance(const Bal
   __shared__ float sums[32];
   __shared__ int live_n;
   const int tid = threadIdx.x, warp = tid >> 5;
-  const bool alone = gridDim.x == 1;
+  const bool alone = gridDim.x == 1 && a.g.t.S <= kAloneSeqs;
   const int t0 = (int)min(a.g.t.T, blockIdx.x * a.per);
   const int t1 = (int)min((uint64_t)a.g.t.T, (uint64_t)t0 + a.per);
   constexpr int U = NC == 1 ? 2 : 1;  // tokens of a team at a time, the next on their way
   const int step = kWarps * (int)tm.per_warp();
-  for (uint32_t s = alone ? 0 : seq_of(a.g.t, t0); s < a.g.t.S; ++s) {
+  for (uint32_t s = alone ? 0 : seq_of(a.g.t, t0), after; s < a.g.t.S; s = after) {
+    after = s + 1;
     const int s0 = seq_at(a.g.t, s), s1 = seq_at(a.g.t, s + 1);
     if (!alone && s0 >= t1) break;
     const int lo = max(s0, t0), hi = min(s1, t1);
-    if (lo >= hi && !alone) continue;
+    if (!alone && lo >= hi) {  // no tokens: to the next that has some
+      after = max(after, seq_of(a.g.t, lo));
+      continue;
+    }
     for (uint32_t e = tid; e < width; e += kThreads) cnt[e] = 0;
     if (tid == 0) live_n = 0;
     __syncthreads();
@@ -666,8 +682,9 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? kBackCtas : NC == 2 ? 2 : 
       // ---- the loss's part
       bool counts = false;
       if (a.count && on) {
-        while (s < a.g.t.S && s_end <= (int)t) {
+        if (s < a.g.t.S && s_end <= (int)t) {
           ++s;
+          if (s < a.g.t.S && seq_at(a.g.t, s + 1) <= (int)t) s = seq_from(a.g.t, s + 1, (int)t);
           if (s < a.g.t.S) {
             s_begin = seq_at(a.g.t, s);
             s_end = seq_at(a.g.t, s + 1);
@@ -916,7 +933,7 @@ cudaError_t launch_balance(const RouterGradArgs &g, int32_t *count, int32_t *tok
   cudaError_t e = g.dt == MOE_DT_F32    ? balance_t<MOE_DT_F32>(a, n, stream)
                   : g.dt == MOE_DT_BF16 ? balance_t<MOE_DT_BF16>(a, n, stream)
                                         : balance_t<MOE_DT_F16>(a, n, stream);
-  if (e != cudaSuccess || n == 1) return e;
+  if (e != cudaSuccess || (n == 1 && g.t.S <= kAloneSeqs)) return e;
   const uint32_t most = 4 * (uint32_t)fp8_ctas(), items = g.t.S * a.chunks;
   return launch_k(k_balance_join, items < most ? items : most, kJoinThreads, 0, stream, true, a);
 }

@@ -106,6 +106,18 @@ def test_balance_of_sequences(rg, T, E, S, fn):
         check_balance(rg, Batch(T, E, 3, S, padded, seed=S), fn)
 
 
+@pytest.mark.parametrize("T,S", [(1, 5), (50, 5000), (700, 65535)])
+def test_many_empty_sequences(rg, T, S):
+    """Runs of empty sequences are passed over (a step each would take tens of ms here)."""
+    b = Batch(T, 16, 2, S, seed=S)
+    check_balance(rg, b, 0)
+    check_backward(rg, b, 0, True)
+    b.seq = np.sort(np.concatenate([np.full(S // 2, T // 3), np.full(S - S // 2, T // 2), [T]]))
+    b.seq = b.seq.astype(np.int32)  # all of them between two tokens
+    check_balance(rg, b, 2)
+    check_backward(rg, b, 2, False)
+
+
 def test_balance_without_tokens(rg):
     b = Batch(20, 16, 2, 4, True)
     b.live[:] = 0
