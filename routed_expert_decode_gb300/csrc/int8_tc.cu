@@ -647,6 +647,64 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
   }
 }
 
+// What the tiles take by the rows of an expert, on average: 32 experts, gate/up 4096 -> 2 x 2048
+// and down 2048 -> 4096, a router's spread of rows (us):
+//   rows            8        16        32        64        96       128       192       512
+//   tile  32    87  49   95  53   116  65   189 105   264 146   335 185   480 263  1208 659
+//         64    88  50   92  53   107  62   137  80   184 107   230 133   320 185   760 440
+//        128   106  57  109  58   115  63   143  78   168  92   194 105   270 145   594 316
+//   256 pair   145  78  146  79   150  83   157  90   171 100   187 113   217 133   427 256
+//
+// The choice goes by a sum of what these and calls of fewer tiles measured: a call takes a
+// fixed time and, for each round of tiles over the SMs (pairs), so much a step of 64 along K
+// and a tile's end.  One expert's rows are known here, and its rounds counted; its pairs' tiles
+// are cut to a height that fills the last round (4000 rows, 4096 channels: 18 of 224 rows).  Of
+// several experts the average is: each has half a tile more than its share of the rows, and
+// some have two where that is about one.
+// 24 experts of 351 rows, K 3328, f 176: 37 us, 47 with the tile by rows alone; 4 of 1550, K
+// 2592, 128 channels: 13 and 25.
+struct Plan {
+  int tile = 0, rows = 0;  // NT (256: pairs) and the rows of a tile
+  Plan(const Fp8Args &a, bool swiglu, int sms) {
+    const double steps = (a.K + 63) / 64, R = a.R, live = a.R < a.E ? a.R : a.E;
+    double least = 1e30;
+    auto take = [&](int nt, int height, uint32_t columns, int workers, double fixed, double step,
+                    double end) {
+      double each = 1;  // tiles of an expert's rows
+      if (a.E == 1) {
+        each = (a.R + height - 1) / height;
+      } else {
+        const double full = R / (live * height);
+        if (0.75 + 0.75 * full > each) each = 0.75 + 0.75 * full;
+        if (full + 0.5 > each) each = full + 0.5;
+      }
+      const double tiles = live * each * ((a.N + columns - 1) / columns);
+      const double x = tiles / workers;
+      const double rounds = x <= 1 ? 1 : x < 3 ? (double)(int)(x + 0.999) : x + 0.5;
+      double us = fixed + rounds * (steps * step + end);
+      // a last round shared along K (run_tc)
+      if (nt == 32 && x < split_share((uint32_t)steps) && us > fixed + x * steps * step + 9.5)
+        us = fixed + x * steps * step + 9.5;
+      if (us < least) {
+        least = us;
+        tile = nt;
+        rows = height;
+      }
+    };
+    const uint32_t channels = swiglu ? 64 : 128;
+    take(32, 32, channels, sms, 4.2, 0.185, 0.5);
+    take(64, 64, channels, sms, 4.6, 0.20, 0.5);
+    take(128, 128, channels, sms, 4.5, 0.30, 0.3);
+    if (sms > 1)
+      for (int h = 256; h >= (a.E == 1 ? 128 : 256); h -= 32)
+        take(256, h, 2 * channels, sms / 2, 3.5, 0.35 * (h + 24) / 280, 3.5);
+  }
+  // A last round of fewer tiles than this part of the SMs is shared along K: a meeting costs
+  // ~9.5 us, the time of some 55 steps (16 rows, 4096 channels, K 6144: 16.9 us, 20 whole; 128
+  // rows, 1024 features, K 4096: 18.6 and 15.8).
+  static double split_share(uint32_t steps) { return steps > 55 ? 1.0 - 55.0 / steps : 0.0; }
+};
+
 template <bool SWIGLU, int NT, bool PAIR>
 cudaError_t run_tc(Fp8Args &a, cudaStream_t stream, int tile_rows = NT) {
   using S = Shape<NT, PAIR>;
@@ -668,9 +726,7 @@ cudaError_t run_tc(Fp8Args &a, cudaStream_t stream, int tile_rows = NT) {
   static std::atomic<bool> done[kMaxDevices];
   const cudaError_t e = allow_smem(kern, done);
   if (e != cudaSuccess) return e;
-  // A last round of few tiles of a long K is shared along K: a meeting costs ~5 us (16 rows,
-  // 4096 channels, K 6144: 16.9 us, 20 whole; 64 rows, 2048 channels, K 2048: 13.0 and 10).
-  const int split_below = S::split && a.nbk >= 32 ? sms / 4 : 0;
+  const int split_below = S::split ? (int)(sms * Plan::split_share(2 * a.nbk)) : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = sms;
   cfg.blockDim = S::threads;
@@ -687,55 +743,13 @@ cudaError_t run_tc(Fp8Args &a, cudaStream_t stream, int tile_rows = NT) {
   return cudaLaunchKernelEx(&cfg, kern, a, maps, (uint32_t)n_w, split_below, tile_rows, pairs);
 }
 
-// The call's rows an expert, on average, choose the tile.  32 experts, gate/up 4096 -> 2 x 2048
-// and down 2048 -> 4096, a router's spread of rows (us):
-//   rows            8        16        32        64        96       128       192       512
-//   tile  32    87  49   95  53   116  65   189 105   264 146   335 185   480 263  1208 659
-//         64    88  50   92  53   107  62   137  80   184 107   230 133   320 185   760 440
-//        128   106  57  109  58   115  63   143  78   168  92   194 105   270 145   594 316
-//   256 pair   145  78  146  79   150  83   157  90   171 100   187 113   217 133   427 256
-
-// One expert's rows are known here, so that whole rounds of tiles can be counted: a call's
-// time is about a fixed part and, for each round, so much a step of 64 along K (measured over
-// 64 to 8000 rows, 512 to 4096 channels, K 1024 to 6144; in 10 ns).  A pair's tiles are cut to
-// a height that fills its last round (4000 rows, 4096 channels: 18 of 224 rows).
-struct OneExpert {
-  int tile = 0, rows = 0;  // NT (256: pairs) and the rows of a tile
-  OneExpert(uint32_t R, uint32_t N, uint32_t K, bool swiglu, int sms) {
-    const uint64_t steps = (K + 63) / 64, channels = swiglu ? 64 : 128;
-    uint64_t least = ~0ull;
-    auto take = [&](int nt, int height, uint64_t columns, int workers, uint64_t fixed,
-                    uint64_t step) {
-      const uint64_t tiles = (uint64_t)((R + height - 1) / height) * ((N + columns - 1) / columns);
-      const uint64_t cost = fixed + (tiles + workers - 1) / workers * steps * step;
-      if (cost < least) {
-        least = cost;
-        tile = nt;
-        rows = height;
-      }
-    };
-    take(32, 32, channels, sms, 420, 18);
-    take(64, 64, channels, sms, 460, 20);
-    take(128, 128, channels, sms, 450, 30);
-    for (int h = 256; h >= 128 && sms > 1; h -= 32)
-      take(256, h, 2 * channels, sms / 2, 650, (uint64_t)(h + 24) / 8);
-  }
-};
-
 template <bool SWIGLU>
-cudaError_t run_by_rows(Fp8Args &a, cudaStream_t stream) {
-  const uint64_t R = a.R, E = a.E;
-  if (E == 1) {
-    const OneExpert best(a.R, a.N, a.K, SWIGLU, fp8_ctas());
-    if (best.tile == 32) return run_tc<SWIGLU, 32, false>(a, stream);
-    if (best.tile == 64) return run_tc<SWIGLU, 64, false>(a, stream);
-    if (best.tile == 128) return run_tc<SWIGLU, 128, false>(a, stream);
-    return run_tc<SWIGLU, 256, true>(a, stream, best.rows);
-  }
-  if (R <= (SWIGLU ? 12 : 20) * E) return run_tc<SWIGLU, 32, false>(a, stream);
-  if (R <= (SWIGLU ? 72 : 56) * E) return run_tc<SWIGLU, 64, false>(a, stream);
-  if (R <= (SWIGLU ? 104 : 144) * E) return run_tc<SWIGLU, 128, false>(a, stream);
-  return run_tc<SWIGLU, 256, true>(a, stream);
+cudaError_t run_planned(Fp8Args &a, cudaStream_t stream) {
+  const Plan plan(a, SWIGLU, fp8_ctas());
+  if (plan.tile == 32) return run_tc<SWIGLU, 32, false>(a, stream);
+  if (plan.tile == 64) return run_tc<SWIGLU, 64, false>(a, stream);
+  if (plan.tile == 128) return run_tc<SWIGLU, 128, false>(a, stream);
+  return run_tc<SWIGLU, 256, true>(a, stream, plan.rows);
 }
 
 }  // namespace
@@ -752,7 +766,7 @@ size_t int8_tc_ws(uint32_t rows) {
 }
 
 cudaError_t launch_int8_tc(Fp8Args &a, bool swiglu, cudaStream_t stream) {
-  return swiglu ? run_by_rows<true>(a, stream) : run_by_rows<false>(a, stream);
+  return swiglu ? run_planned<true>(a, stream) : run_planned<false>(a, stream);
 }
 
 }  // namespace moe
