@@ -661,8 +661,8 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
 // are cut to a height that fills the last round (4000 rows, 4096 channels: 18 of 224 rows).  Of
 // several experts the average is: each has half a tile more than its share of the rows, and
 // some have two where that is about one.
-// 24 experts of 351 rows, K 3328, f 176: 37 us, 47 with the tile by rows alone; 4 of 1550, K
-// 2592, 128 channels: 13 and 25.
+// 24 experts of 351 rows, K 3328, f 176: 38 us, 47 with the tile by rows alone; 4 of 1550, K
+// 2592, 128 channels: 15 and 25.
 struct Plan {
   int tile = 0, rows = 0;  // NT (256: pairs) and the rows of a tile
   Plan(const Fp8Args &a, bool swiglu, int sms) {

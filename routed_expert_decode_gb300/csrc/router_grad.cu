@@ -10,7 +10,7 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kBackCtas = 3;  // CTAs an SM of the logits' gradient (65536 x 256 bf16: 38 us, 40 with 4, 44 with 2)
+constexpr int kBackCtas = 3;  // CTAs an SM of the logits' gradient (65536 x 256 bf16: 35 us, 37 with 4)
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -558,8 +558,9 @@ __device__ __forceinline__ void store_row(const RouteBackArgs &a, uint32_t t, co
 // their part of the gradient goes to rows of zeros in shared memory.  Then the tokens, each
 // by its team, the next one's logits on their way: scores, the loss's part (whose
 // coefficients stay in registers from token to token), the picks' part from shared memory.
-// 65536 x 256 bf16, top 8, with the loss: 37.7 us (39.1 with the picks token by token, from p
-// laid out in shared memory), of which scores and stores alone are 20; bound by issue.
+// 65536 x 256 bf16, top 8, with the loss: 35.0 us, of which scores and stores alone are some 20
+// (with longer runs for fewer CTAs 37.7, and 39.1 with the picks token by token, from p laid out
+// in shared memory); bound by issue and the latency between a token's sums.
 template <int DT, int NC, bool WIDE>
 __global__ void __launch_bounds__(kThreads, NC == 1 ? kBackCtas : NC == 2 ? 2 : 1)
     k_route_backward(const RouteBackArgs a) {
@@ -955,11 +956,12 @@ cudaError_t launch_route_backward(const RouterGradArgs &g, const float *dw, cons
   a.ldd = ldd;
   a.slots = 8;  // four tokens a batch: its rows of zeros are that many
   while (a.slots < g.r.top_k) a.slots *= 2;
-  // as many warps as run at a time, whole batches each
-  const uint32_t nt = 32 / a.lanes, nb = 32 / a.slots, batch = nb > nt ? nb : nt;
-  const uint64_t batches = ((uint64_t)g.t.T + batch - 1) / batch;
+  // As many warps as run at a time, with equal runs: whole batches each would leave every tenth
+  // CTA out (65536 tokens: 410 of 456; 37.7 us in place of 35.0).
+  const uint32_t nt = 32 / a.lanes;
+  const uint64_t groups = ((uint64_t)g.t.T + nt - 1) / nt;  // of a team's tokens
   const uint64_t warps = (uint64_t)fp8_ctas() * kBackCtas * kWarps;
-  a.run = (uint32_t)((batches + warps - 1) / warps) * batch;
+  a.run = (uint32_t)((groups + warps - 1) / warps) * nt;
   const unsigned grid =
       (unsigned)(((uint64_t)g.t.T + (uint64_t)a.run * kWarps - 1) / ((uint64_t)a.run * kWarps));
   if (g.dt == MOE_DT_F32) return route_backward_t<MOE_DT_F32>(a, grid, stream);
