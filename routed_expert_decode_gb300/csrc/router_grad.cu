@@ -10,7 +10,7 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kBackCtas = 3;  // CTAs an SM of the logits' gradient (65536 x 256 bf16: 35 us, 37 with 4)
+constexpr int kBackCtas = 3;  // CTAs an SM of the logits' gradient (65536 x 256 bf16: 33 us, 34 with 4)
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -253,7 +253,7 @@ __device__ __forceinline__ uint32_t seq_from(const moe_tokens &t, uint32_t s, in
 // before or behind, the sums go to the workspace (the first slot if the sequence begins
 // before the CTA's tokens, the second if it begins among them: at most one each), where
 // k_balance_join adds them in order.
-constexpr uint32_t kSumCtas = 4;      // an SM, at most (65536 x 256 bf16: 30 us; 34 with 6, 31 with 3)
+constexpr uint32_t kSumCtas = 3;  // an SM, at most (65536 x 256 bf16, 16 sequences: 24 us; 26 with 2 or 4)
 constexpr uint32_t kSumPasses = 4;  // tokens of a team, at least
 constexpr uint32_t kJoinRun = 32;   // experts of a joining CTA
 constexpr uint32_t kAloneSeqs = 4;  // sequences of a call that one CTA finishes, at most
@@ -309,7 +309,7 @@ __device__ __forceinline__ void finish_loss(const BalanceArgs &a, float *red) {
 }
 
 template <int DT, int NC, bool WIDE>
-__global__ void __launch_bounds__(kThreads, NC == 1 ? 4 : 2) k_balance(const BalanceArgs a) {
+__global__ void __launch_bounds__(kThreads, NC == 1 ? kSumCtas : 2) k_balance(const BalanceArgs a) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ __align__(16) uint8_t bsm[];
@@ -536,14 +536,14 @@ struct RouteBackArgs {
 
 template <int OT, int NC, typename Team>
 __device__ __forceinline__ void store_row(const RouteBackArgs &a, uint32_t t, const Team &tm,
-                                          const float2 (&d2)[NC][4]) {
+                                          bool vec, const float2 (&d2)[NC][4]) {
   typename Elem<OT>::T *row = (typename Elem<OT>::T *)a.dlogits + (size_t)t * a.ldd;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const uint32_t e = tm.expert(c);
     const float d[8] = {d2[c][0].x, d2[c][0].y, d2[c][1].x, d2[c][1].y,
                         d2[c][2].x, d2[c][2].y, d2[c][3].x, d2[c][3].y};
-    if (a.vec_out) {
+    if (vec) {
       if (e < a.g.r.n_expert) store8<OT>(row + e, d);
     } else {
 #pragma unroll
@@ -558,16 +558,21 @@ __device__ __forceinline__ void store_row(const RouteBackArgs &a, uint32_t t, co
 // their part of the gradient goes to rows of zeros in shared memory.  Then the tokens, each
 // by its team, the next one's logits on their way: scores, the loss's part (whose
 // coefficients stay in registers from token to token), the picks' part from shared memory.
-// 65536 x 256 bf16, top 8, with the loss: 35.0 us, of which scores and stores alone are some 20
-// (with longer runs for fewer CTAs 37.7, and 39.1 with the picks token by token, from p laid out
-// in shared memory); bound by issue and the latency between a token's sums.
-template <int DT, int NC, bool WIDE>
+// FAST: sigmoid, whole chunks of 8 in and out, the gradient of the logits' type, known when
+// compiling.
+// 65536 x 256 bf16, top 8, with the loss: 33.0 us, of which scores and stores alone are some
+// 20.  35.0 without FAST, and then 37.7 with longer runs for fewer CTAs, 39.1 with the picks
+// token by token, from p laid out in shared memory.  Bound by issue and a token's sums.
+template <int DT, int NC, bool WIDE, bool FAST>
 __global__ void __launch_bounds__(kThreads, NC == 1 ? kBackCtas : NC == 2 ? 2 : 1)
     k_route_backward(const RouteBackArgs a) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ __align__(16) uint8_t rsm[];
-  const uint32_t E = a.g.r.n_expert, k = a.g.r.top_k, fn = a.g.r.score, T = a.g.t.T;
+  const uint32_t E = a.g.r.n_expert, k = a.g.r.top_k, T = a.g.t.T;
+  const uint32_t fn = FAST ? MOE_SCORE_SIGMOID : a.g.r.score;
+  const int odt = FAST ? DT : a.odt;
+  const bool vec = FAST || a.vec, vec_out = FAST || a.vec_out;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Team<WIDE> tm(a.lanes);
   const uint32_t width = NC * tm.lanes() * 8, nt = tm.per_warp();
@@ -652,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? kBackCtas : NC == 2 ? 2 : 
   Row<DT, NC> next;
   bool next_live = true;
   auto fetch = [&](uint32_t x) {
-    next.load(a.g.logits, a.g.ld, x, E, tm, a.vec, x < t1);
+    next.load(a.g.logits, a.g.ld, x, E, tm, vec, x < t1);
     if (a.count && a.g.t.live) next_live = x < t1 && a.g.t.live[x];
   };
   fetch(t0 + tm.t);
@@ -755,9 +760,9 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? kBackCtas : NC == 2 ? 2 : 
 #pragma unroll
         for (int j = 0; j < 4; ++j) d[c][j] = mul2(d[c][j], slope[c][j]);
       if (!on) continue;
-      if (a.odt == MOE_DT_F32) store_row<MOE_DT_F32, NC>(a, t, tm, d);
-      else if (a.odt == MOE_DT_BF16) store_row<MOE_DT_BF16, NC>(a, t, tm, d);
-      else store_row<MOE_DT_F16, NC>(a, t, tm, d);
+      if (odt == MOE_DT_F32) store_row<MOE_DT_F32, NC>(a, t, tm, vec_out, d);
+      else if (odt == MOE_DT_BF16) store_row<MOE_DT_BF16, NC>(a, t, tm, vec_out, d);
+      else store_row<MOE_DT_F16, NC>(a, t, tm, vec_out, d);
     }
     if (!a.dw) continue;
     __syncwarp();
@@ -875,11 +880,13 @@ cudaError_t route_backward_t(const RouteBackArgs &a, unsigned grid, cudaStream_t
     const cudaError_t e = allow_smem(kern, done);
     return e != cudaSuccess ? e : launch_k(kern, grid, kThreads, smem, stream, true, a);
   };
-  static std::atomic<bool> done[4][kMaxDevices];
-  if (a.lanes < 32) return run(k_route_backward<DT, 1, false>, done[0]);
-  if (nc == 1) return run(k_route_backward<DT, 1, true>, done[1]);
-  if (nc == 2) return run(k_route_backward<DT, 2, true>, done[2]);
-  return run(k_route_backward<DT, 4, true>, done[3]);
+  static std::atomic<bool> done[5][kMaxDevices];
+  if (a.lanes < 32) return run(k_route_backward<DT, 1, false, false>, done[0]);
+  if (nc == 1 && a.g.r.score == MOE_SCORE_SIGMOID && a.vec && a.vec_out && a.odt == DT)
+    return run(k_route_backward<DT, 1, true, true>, done[1]);
+  if (nc == 1) return run(k_route_backward<DT, 1, true, false>, done[2]);
+  if (nc == 2) return run(k_route_backward<DT, 2, true, false>, done[3]);
+  return run(k_route_backward<DT, 4, true, false>, done[4]);
 }
 
 template <int DT, int YT>
