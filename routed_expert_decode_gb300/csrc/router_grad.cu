@@ -93,11 +93,10 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
-// e^-x for |x| up to 110 (0 at 110, infinite below -88.7): the square of 2^(-x/2 log2 e) by
-// the special function unit, so that a subnormal result is not flushed, with the
-// roundings of the product and of log2 e made good, as those of an argument of 80 would
-// be 80 ulp.  Within 4 ulp.
-__device__ __forceinline__ float2 exp_of_minus(float2 x) {
+// e^(-x/2) for |x| up to 180 (0 at 180): 2^(-x/2 log2 e) by the special function unit, with
+// the roundings of the product and of log2 e made good, as those of an argument of 80
+// would be 40 ulp.  Within 2 ulp.
+__device__ __forceinline__ float2 exp_of_minus_half(float2 x) {
   constexpr float kHi = 1.4426950216293335f, kLo = 1.9259629911266175e-8f;  // log2 e
   constexpr float kLn2 = 0.6931471805599453f;
   const float2 t = mul2(x, both(0.5f * kHi));
@@ -106,8 +105,13 @@ __device__ __forceinline__ float2 exp_of_minus(float2 x) {
   float2 e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(-t.x));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(-t.y));
-  e = fma2(mul2(e, both(kLn2)), rest, e);
-  return mul2(e, e);
+  return fma2(mul2(e, both(kLn2)), rest, e);
+}
+// e^-x for |x| up to 110 (0 at 110, infinite below -88.7): a square, so that a subnormal
+// result is not flushed.  Within 4 ulp.
+__device__ __forceinline__ float2 exp_of_minus(float2 x) {
+  const float2 h = exp_of_minus_half(x);
+  return mul2(h, h);
 }
 // 1 / x within an ulp; 0 for x above 2^126
 __device__ __forceinline__ float2 rcp2(float2 x) {
@@ -115,6 +119,34 @@ __device__ __forceinline__ float2 rcp2(float2 x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(x.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(x.y));
   return r;
+}
+
+// sqrt(log(1 + e^l)), and its slope's d log / dl = sigmoid(l) / (2 log(1 + e^l)), of two l.
+// With e = e^-|l|, log(1 + e) = e q, where q = 2/(2+e) (1 + z/3 + z^2/5 + ...) of z =
+// (e/(2+e))^2 <= 1/9 is the series of 2 artanh(e/(2+e)), cut where 1.5e-8 is left.  Below 0 the
+// root is e^(-|l|/2) sqrt(q) and the slope 1 / (2 (1+e) q), so that neither underflows before
+// the root itself does; from 0 on they are of l + e q.  Both within 6 ulp.
+template <bool SLOPE>
+__device__ __forceinline__ float2 softplus_root(float2 l, float2 &slope) {
+  const float2 h = exp_of_minus_half(
+      make_float2(fminf(fabsf(l.x), 180.0f), fminf(fabsf(l.y), 180.0f)));
+  const float2 e = mul2(h, h), r = rcp2(add2(e, both(2.0f)));
+  const float2 t = mul2(e, r), z = mul2(t, t);
+  float2 q = fma2(z, both(1.0f / 13), both(1.0f / 11));
+  q = fma2(q, z, both(1.0f / 9));
+  q = fma2(q, z, both(1.0f / 7));
+  q = fma2(q, z, both(1.0f / 5));
+  q = fma2(q, z, both(1.0f / 3));
+  q = mul2(fma2(q, z, both(1.0f)), add2(r, r));
+  const bool ux = l.x >= 0.0f, uy = l.y >= 0.0f;  // NaN: as -inf
+  const float2 up = fma2(e, q, make_float2(fminf(l.x, FLT_MAX), fminf(l.y, FLT_MAX)));
+  const float2 v = make_float2(ux ? up.x : q.x, uy ? up.y : q.y);
+  float2 root;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(root.x) : "f"(v.x));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(root.y) : "f"(v.y));
+  if (SLOPE)
+    slope = mul2(mul2(mul2(rcp2(add2(e, both(1.0f))), both(0.5f)), root), root);
+  return mul2(mul2(v, root), make_float2(ux ? 1.0f : h.x, uy ? 1.0f : h.y));
 }
 
 // l -> scores p (softmax: whose sum is 1), in place; slope = d log p / dl, softmax's
@@ -182,20 +214,8 @@ __device__ __forceinline__ float scores(uint32_t fn, const Team &tm, float2 (&l)
   for (int c = 0; c < NC; ++c)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 e = exp_of_minus(
-          make_float2(fminf(fabsf(l[c][i].x), 110.0f), fminf(fabsf(l[c][i].y), 110.0f)));
-      const float2 big = rcp2(add2(e, both(1.0f))), small = mul2(e, big);
-      auto one = [](float v, float e, float b, float m, float &g) {
-        const float soft = fminf(fmaxf(v, 0.0f), FLT_MAX) + log1pf(e);
-        // sigmoid / (2 softplus); 1/2 in the limit of -inf
-        if (SLOPE) g = soft > 0.0f ? __fdiv_rn(0.5f * (v >= 0.0f ? b : m), soft) : 0.5f;
-        return __fsqrt_rn(soft);
-      };
-      float2 &v = l[c][i], &g = slope[c][i];
-      float gx = 0.0f, gy = 0.0f;
-      v.x = one(v.x, e.x, big.x, small.x, gx);
-      v.y = one(v.y, e.y, big.y, small.y, gy);
-      if (SLOPE) g = make_float2(gx, gy);
+      float2 &v = l[c][i];
+      v = softplus_root<SLOPE>(v, slope[c][i]);
       s = add2(s, v);
     }
   return tm.sum(s.x + s.y);
@@ -204,12 +224,13 @@ __device__ __forceinline__ float scores(uint32_t fn, const Team &tm, float2 (&l)
 // p of one logit; softmax: e^(l - top), and 0 for -inf whatever top is
 __device__ __forceinline__ float score_of(uint32_t fn, float l, float top) {
   if (fn == MOE_SCORE_SOFTMAX) return exp_of_minus(both(fminf(top - l, 110.0f))).x;
-  const float e = exp_of_minus(both(fminf(fabsf(l), 110.0f))).x;
   if (fn == MOE_SCORE_SIGMOID) {
+    const float e = exp_of_minus(both(fminf(fabsf(l), 110.0f))).x;
     const float big = rcp2(both(1.0f + e)).x;
     return l >= 0.0f ? big : e * big;
   }
-  return __fsqrt_rn(fminf(fmaxf(l, 0.0f), FLT_MAX) + log1pf(e));
+  float2 none;
+  return softplus_root<false>(both(l), none).x;
 }
 
 // ---------------------------------------------------------------- sequences

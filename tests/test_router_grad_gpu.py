@@ -150,6 +150,23 @@ def test_special_logits(rg, fn):
         check_backward(rg, b, fn, renorm)
 
 
+@pytest.mark.parametrize("fn", [0, 1])
+@pytest.mark.parametrize("E", [24, 256])
+def test_wide_logits(rg, fn, E):
+    """Rows from one end of the scores' range to the other, and rows of its ends alone."""
+    b = Batch(48, E, 6, 2, True, seed=14)
+    g = np.random.default_rng(15)
+    least = -170.0 if fn else -80.0   # whose score is not below the smallest normal float
+    l = g.uniform(least, 100.0, (48, E))
+    l[:12] = g.uniform(least, least + 40, (12, E))
+    l[12:24] = g.uniform(-2.0, 2.0, (12, E))
+    l[24:30] = g.uniform(60.0, 100.0, (6, E))
+    b.logits = dev(l.astype(np.float32))
+    check_balance(rg, b, fn)
+    for renorm in (True, False):
+        check_backward(rg, b, fn, renorm)
+
+
 def test_balance_strides_picks_and_repeats(rg):
     b = Batch(500, 64, 4, 6, True, dt="bf16", seed=8)
     b.idx[::7, 1] = -1          # picks that are none
