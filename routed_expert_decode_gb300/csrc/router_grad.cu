@@ -10,7 +10,9 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kBackCtas = 3;  // CTAs an SM of the logits' gradient (65536 x 256 bf16: 33 us, 34 with 4)
+// CTAs an SM of the logits' gradient by a lane's chunks of experts, all of a grid at a time
+// (65536 x 256 bf16: 33 us, 34 with 4; 32768 x 512: 29, and 37 with a grid of 3)
+constexpr int back_ctas(int nc) { return nc == 1 ? 3 : nc == 2 ? 2 : 1; }
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -274,7 +276,8 @@ __device__ __forceinline__ uint32_t seq_from(const moe_tokens &t, uint32_t s, in
 // before or behind, the sums go to the workspace (the first slot if the sequence begins
 // before the CTA's tokens, the second if it begins among them: at most one each), where
 // k_balance_join adds them in order.
-constexpr uint32_t kSumCtas = 3;  // an SM, at most (65536 x 256 bf16, 16 sequences: 24 us; 26 with 2 or 4)
+// an SM, by a lane's chunks of experts (65536 x 256 bf16, 16 sequences: 24 us, 26 with 2 or 4)
+constexpr int sum_ctas(int nc) { return nc == 1 ? 3 : 2; }
 constexpr uint32_t kSumPasses = 4;  // tokens of a team, at least
 constexpr uint32_t kJoinRun = 32;   // experts of a joining CTA
 constexpr uint32_t kAloneSeqs = 4;  // sequences of a call that one CTA finishes, at most
@@ -330,7 +333,7 @@ __device__ __forceinline__ void finish_loss(const BalanceArgs &a, float *red) {
 }
 
 template <int DT, int NC, bool WIDE>
-__global__ void __launch_bounds__(kThreads, NC == 1 ? kSumCtas : 2) k_balance(const BalanceArgs a) {
+__global__ void __launch_bounds__(kThreads, sum_ctas(NC)) k_balance(const BalanceArgs a) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ __align__(16) uint8_t bsm[];
@@ -585,7 +588,7 @@ __device__ __forceinline__ void store_row(const RouteBackArgs &a, uint32_t t, co
 // 20.  35.0 without FAST, and then 37.7 with longer runs for fewer CTAs, 39.1 with the picks
 // token by token, from p laid out in shared memory.  Bound by issue and a token's sums.
 template <int DT, int NC, bool WIDE, bool FAST>
-__global__ void __launch_bounds__(kThreads, NC == 1 ? kBackCtas : NC == 2 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, back_ctas(NC))
     k_route_backward(const RouteBackArgs a) {
   pdl_trigger();
   pdl_wait();
@@ -901,13 +904,14 @@ cudaError_t route_backward_t(const RouteBackArgs &a, unsigned grid, cudaStream_t
     const cudaError_t e = allow_smem(kern, done);
     return e != cudaSuccess ? e : launch_k(kern, grid, kThreads, smem, stream, true, a);
   };
-  static std::atomic<bool> done[5][kMaxDevices];
+  static std::atomic<bool> done[6][kMaxDevices];
+  const bool fast = a.g.r.score == MOE_SCORE_SIGMOID && a.vec && a.vec_out && a.odt == DT;
   if (a.lanes < 32) return run(k_route_backward<DT, 1, false, false>, done[0]);
-  if (nc == 1 && a.g.r.score == MOE_SCORE_SIGMOID && a.vec && a.vec_out && a.odt == DT)
-    return run(k_route_backward<DT, 1, true, true>, done[1]);
+  if (nc == 1 && fast) return run(k_route_backward<DT, 1, true, true>, done[1]);
   if (nc == 1) return run(k_route_backward<DT, 1, true, false>, done[2]);
-  if (nc == 2) return run(k_route_backward<DT, 2, true, false>, done[3]);
-  return run(k_route_backward<DT, 4, true, false>, done[4]);
+  if (nc == 2 && fast) return run(k_route_backward<DT, 2, true, true>, done[3]);
+  if (nc == 2) return run(k_route_backward<DT, 2, true, false>, done[4]);
+  return run(k_route_backward<DT, 4, true, false>, done[5]);
 }
 
 template <int DT, int YT>
@@ -929,7 +933,8 @@ cudaError_t combine_backward_from(int ydt, const CombineBackArgs &a, cudaStream_
 
 uint32_t balance_ctas(uint32_t T, uint32_t E) {
   const uint32_t least = kWarps * (32 / team_lanes(E)) * kSumPasses;  // tokens of a CTA
-  const uint32_t n = (T + least - 1) / least, most = kSumCtas * (uint32_t)fp8_ctas();
+  const uint32_t n = (T + least - 1) / least;
+  const uint32_t most = (uint32_t)(sum_ctas(chunks_of(E)) * fp8_ctas());
   return n < 1 ? 1 : n < most ? n : most;
 }
 
@@ -988,7 +993,7 @@ cudaError_t launch_route_backward(const RouterGradArgs &g, const float *dw, cons
   // CTA out (65536 tokens: 410 of 456; 37.7 us in place of 35.0).
   const uint32_t nt = 32 / a.lanes;
   const uint64_t groups = ((uint64_t)g.t.T + nt - 1) / nt;  // of a team's tokens
-  const uint64_t warps = (uint64_t)fp8_ctas() * kBackCtas * kWarps;
+  const uint64_t warps = (uint64_t)fp8_ctas() * back_ctas(chunks_of(g.r.n_expert)) * kWarps;
   a.run = (uint32_t)((groups + warps - 1) / warps) * nt;
   const unsigned grid =
       (unsigned)(((uint64_t)g.t.T + (uint64_t)a.run * kWarps - 1) / ((uint64_t)a.run * kWarps));
