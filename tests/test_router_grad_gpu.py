@@ -228,6 +228,29 @@ def test_route_backward_of_sequences(rg, T, E, S):
         check_backward(rg, Batch(T, E, 3, S, padded, seed=S), 0, True)
 
 
+@pytest.mark.parametrize("fn", [0, 2])
+@pytest.mark.parametrize("E", [20, 64, 256, 384, 1000])
+def test_route_backward_of_many_tokens(rg, E, fn):
+    """Warps with many tokens each: every row is what a call of a few hundred tokens gives."""
+    T, k, S = 120007 if E < 256 else 30011, 5, 9
+    g = torch.Generator("cuda").manual_seed(E)
+    logits = torch.randn((T, E), generator=g, device="cuda").to(torch.bfloat16)
+    idx = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    dw = torch.randn((T, k), generator=g, device="cuda")
+    live = (torch.rand(T, generator=g, device="cuda") > 0.2).to(torch.uint8)
+    seq = dev(np.sort(np.random.default_rng(E).integers(0, T + 1, S + 1)).astype(np.int32))
+    counts = torch.randint(0, 900, (S, E), generator=g, device="cuda", dtype=torch.int32)
+    tokens = torch.randint(1, 9000, (S,), generator=g, device="cuda", dtype=torch.int32)
+    r, got = router(E, k, fn), torch.empty_like(logits)
+    rg.route_backward(r, logits, idx, got, dw, counts, tokens, seq=seq, live=live, coef=0.5)
+    for a in range(0, T, T // 6):
+        n = min(777, T - a)
+        few = torch.empty((n, E), dtype=torch.bfloat16, device="cuda")
+        rg.route_backward(r, logits[a:a + n], idx[a:a + n], few, dw[a:a + n], counts, tokens,
+                          seq=(seq - a).clamp(0, n), live=live[a:a + n], coef=0.5)
+        assert torch.equal(got[a:a + n], few), a
+
+
 def test_route_backward_strides_types_and_picks(rg):
     b = Batch(90, 64, 6, 3, True, seed=8, spread=3.0)
     b.idx[::7, 1] = -1
