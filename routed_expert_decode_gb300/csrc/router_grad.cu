@@ -223,6 +223,12 @@ __device__ __forceinline__ float scores(uint32_t fn, const Team &tm, float2 (&l)
   return tm.sum(s.x + s.y);
 }
 
+// Scores that add up to less than this are taken 2^64 times, which is exact: the reciprocal
+// of their sum may be infinite otherwise (a sum below 2^-128), and products with them lose
+// bits as subnormal numbers.
+constexpr float kTinySum = 0x1p-64f, kTinyScale = 0x1p64f;
+__device__ __forceinline__ bool tiny_sum(float sum) { return sum > 0.0f && sum < kTinySum; }
+
 // p of one logit; softmax: e^(l - top), and 0 for -inf whatever top is
 __device__ __forceinline__ float score_of(uint32_t fn, float l, float top) {
   if (fn == MOE_SCORE_SOFTMAX) return exp_of_minus(both(fminf(top - l, 110.0f))).x;
@@ -652,11 +658,17 @@ __global__ void __launch_bounds__(kThreads, back_ctas(NC))
         top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
       top = fmaxf(top, -FLT_MAX);
     }
-    const float p = e < E ? score_of(fn, l, top) : 0.0f;
-    const float dots = group_sum(p * g);
+    float p = e < E ? score_of(fn, l, top) : 0.0f;
+    float dots = group_sum(p * g);
     float v = a.g.r.s * p * g;
     if (a.g.r.renorm) {
-      const float total = group_sum(p);
+      float total = group_sum(p);
+      if (__any_sync(kAll, tiny_sum(total))) {
+        const float f = tiny_sum(total) ? kTinyScale : 1.0f;
+        p *= f;
+        total *= f;
+        dots = group_sum(p * g);
+      }
       const float inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
       v = a.g.r.s * (p * inv) * (g - dots * inv);
     }
@@ -708,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, back_ctas(NC))
       next.to(p);
       if (b0 + i + nt < t1) fetch(t + nt);
       float top = 0.0f, norm = 0.0f;
-      const float sum = scores<NC, true>(fn, tm, p, slope, top, norm);
+      float sum = scores<NC, true>(fn, tm, p, slope, top, norm);
       // ---- the loss's part
       bool counts = false;
       if (a.count && on) {
@@ -736,13 +748,26 @@ __global__ void __launch_bounds__(kThreads, back_ctas(NC))
         }
       }
       if (__any_sync(kAll, counts)) {
+        auto weighted = [&]() {  // sum of coef p
+          float2 dots = both(0.0f);
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dots = fma2(coef[c][j], p[c][j], dots);
+          return tm.sum(dots.x + dots.y);
+        };
+        float dot = weighted();
+        if (__any_sync(kAll, tiny_sum(sum))) {
+          const float f = tiny_sum(sum) ? kTinyScale : 1.0f;
+          sum *= f;
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[c][j] = mul2(p[c][j], both(f));
+          dot = weighted();
+        }
         const float inv = counts && sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-        float2 dots = both(0.0f);
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) dots = fma2(coef[c][j], p[c][j], dots);
-        const float dot = tm.sum(dots.x + dots.y) * inv;
+        dot *= inv;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
