@@ -9,7 +9,9 @@
  *
  * Notation: E, k, s, scores p_e of a token's logits and weights w_j of its picks as
  * moe_group_route defines them (moe_router; its groups play no part here, and what
- * it does with NaN and infinite logits holds here too);
+ * it does with NaN and infinite logits holds here too; its sigmoid is 0 below -88.72283,
+ * and so is p_e; its sqrt(softplus), whose e^l is a subnormal number from -87 and 0 from
+ * -103.97 down, is here that of the exact e^l down to -174);
  *   share_e = p_e (softmax) or p_e / sum_e p_e, 0 where the sum is 0.
  *
  * Sequences: seq [S+1] ascending token offsets in [0, T]; sequence i's tokens are

@@ -153,7 +153,8 @@ __device__ __forceinline__ float2 softplus_root(float2 l, float2 &slope) {
 
 // l -> scores p (softmax: whose sum is 1), in place; slope = d log p / dl, softmax's
 // without its sum's part.  A NaN counts as -inf, +inf as the largest finite value.
-// Returns the sum of p; top and norm: softmax's maximum of l and the factor of e^(l - top).
+// Returns the sum of p (without SLOPE, sigmoid's p and sum are four times those); top and norm:
+// softmax's maximum of l and the factor of e^(l - top).
 template <int NC, bool SLOPE, typename Team>
 __device__ __forceinline__ float scores(uint32_t fn, const Team &tm, float2 (&l)[NC][4],
                                         float2 (&slope)[NC][4], float &top, float &norm) {
@@ -206,7 +207,8 @@ __device__ __forceinline__ float scores(uint32_t fn, const Team &tm, float2 (&l)
         } else {
           const float2 e = exp_of_minus(make_float2(fminf(fmaxf(v.x, -110.0f), 110.0f),
                                                     fminf(fmaxf(v.y, -110.0f), 110.0f)));
-          l[c][i] = rcp2(add2(e, both(1.0f)));
+          // four times p, which shares do not see: rcp2 is not 0 before e is infinite
+          l[c][i] = rcp2(fma2(e, both(0.25f), both(0.25f)));
         }
         s = add2(s, l[c][i]);
       }
@@ -227,6 +229,11 @@ __device__ __forceinline__ float scores(uint32_t fn, const Team &tm, float2 (&l)
 // of their sum may be infinite otherwise (a sum below 2^-128), and products with them lose
 // bits as subnormal numbers.
 constexpr float kTinySum = 0x1p-64f, kTinyScale = 0x1p64f;
+// The router's sigmoid is 1 / (1 + e^-l), and 0 where e^-l is infinite: at logits below
+// kLeastLogit, whose p are below kLeastScore.  They count as 0 here where it matters: picks, and
+// tokens whose scores are tiny in all.  (sqrt(softplus) goes on as e^(l/2) down to -174.7; the
+// router's has few bits below -87 and is 0 below -103.97.)
+constexpr float kLeastLogit = -88.72283f, kLeastScore = 0x1.00004p-128f;
 __device__ __forceinline__ bool tiny_sum(float sum) { return sum > 0.0f && sum < kTinySum; }
 
 // p of one logit; softmax: e^(l - top), and 0 for -inf whatever top is
@@ -235,7 +242,7 @@ __device__ __forceinline__ float score_of(uint32_t fn, float l, float top) {
   if (fn == MOE_SCORE_SIGMOID) {
     const float e = exp_of_minus(both(fminf(fabsf(l), 110.0f))).x;
     const float big = rcp2(both(1.0f + e)).x;
-    return l >= 0.0f ? big : e * big;
+    return l >= 0.0f ? big : l < kLeastLogit ? 0.0f : e * big;
   }
   float2 none;
   return softplus_root<false>(both(l), none).x;
@@ -758,12 +765,20 @@ __global__ void __launch_bounds__(kThreads, back_ctas(NC))
         };
         float dot = weighted();
         if (__any_sync(kAll, tiny_sum(sum))) {
-          const float f = tiny_sum(sum) ? kTinyScale : 1.0f;
-          sum *= f;
+          const bool tiny = tiny_sum(sum);
+          float2 some = both(0.0f);
 #pragma unroll
           for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) p[c][j] = mul2(p[c][j], both(f));
+            for (int j = 0; j < 4; ++j) {
+              float2 &v = p[c][j];
+              if (tiny)
+                v = make_float2(v.x < kLeastScore ? 0.0f : v.x * kTinyScale,
+                                v.y < kLeastScore ? 0.0f : v.y * kTinyScale);
+              some = add2(some, v);
+            }
+          const float again = tm.sum(some.x + some.y);
+          if (tiny) sum = again;
           dot = weighted();
         }
         const float inv = counts && sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
