@@ -157,8 +157,9 @@ def swiglu(gate: Mat, up: Mat, xq, xs, h, ws, off=None, perm=None, top_k: int = 
 class Layer(fp8.Layer):
     """One routed layer over int8 weights on a device, as ``fp8.Layer``: group-limited routing,
     the experts' SwiGLU and down products, the always-on shared expert, the weighted combine.
-    The weights are this module's ``Mat``; h is held in x's type between its product and its
-    quantiser."""
+    The weights are this module's ``Mat``.  Between its product and its quantiser h is held in
+    x's type, of float16 in float32: silu(g) u passes 65504 where the quantiser's scale and the
+    layer's outputs do not."""
 
     def __init__(self, router, gate, up, down, shared=None, keep_bytes: int = 4 << 30):
         if not all(isinstance(m, Mat) for m in (gate, up, down, *(shared or ()))):
@@ -169,13 +170,14 @@ class Layer(fp8.Layer):
         E, k, d, f, R = self.E, self.router.top_k, self.d, self.f, T * self.router.top_k
         make = self._empty
         i32, f32, i8 = torch.int32, torch.float32, torch.int8
+        h = f32 if dtype is torch.float16 else dtype
         b = dict(idx=make((T, k), i32), w=make((T, k), f32), off=make((E + 1,), i32),
                  perm=make((R,), i32), pos=make((T, k), i32), xq=make((T, d), i8),
-                 xs=make((T,), f32), h=make((R, f), dtype), hq=make((R, f), i8),
+                 xs=make((T,), f32), h=make((R, f), h), hq=make((R, f), i8),
                  hs=make((R,), f32), o=make((R, d), dtype), shared=None)
         if self.shared is not None:
             fs = self.shared[0].N
-            b.update(sh=make((T, fs), dtype), shq=make((T, fs), i8), shs=make((T,), f32),
+            b.update(sh=make((T, fs), h), shq=make((T, fs), i8), shs=make((T,), f32),
                      shared=make((T, d), dtype))
         n = max(group_route_workspace_size(self.router, T), workspace_size(max(R, T)))
         b["ws"] = torch.zeros(n, dtype=torch.uint8, device=self.gate.q.device)

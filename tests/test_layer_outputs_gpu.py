@@ -1,12 +1,11 @@
-"""What a routed layer's call leaves behind: rows beyond half precision's range, and outputs whose
-buffers a later call has taken."""
+"""A routed layer of half precision whose rows between the products pass its range."""
 import numpy as np
 import pytest
 import torch
 
 import fp8_ref
 from test_int8_gpu import dev
-from test_int8_layer_gpu import check_experts, int8, make_layer, make_mat  # noqa: F401
+from test_int8_layer_gpu import check_experts, int8, make_layer  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
