@@ -301,7 +301,7 @@ def combine(o, w, pos, y, shared=None, stream=None) -> None:
 @dataclass
 class LayerOutput:
     """What a layer call computed: its result and the buffers it went through (their
-    values are valid until the layer's next call with as many tokens)."""
+    values are valid until the layer's next call with as many tokens of the type)."""
     y: torch.Tensor
     idx: torch.Tensor
     w: torch.Tensor
@@ -314,6 +314,12 @@ class LayerOutput:
     hs: torch.Tensor
     o: torch.Tensor
     shared: Optional[torch.Tensor]
+    call: Optional[tuple] = None  # the buffers' counter of calls, and what it was at this one
+
+    @property
+    def stale(self) -> bool:
+        """Whether a later call of the layer has taken the buffers (a replayed graph is not seen)."""
+        return self.call is not None and self.call[0][0] != self.call[1]
 
 
 class Layer:
@@ -345,6 +351,7 @@ class Layer:
         self.E, self.f, self.d = gate.E, gate.N, gate.K
         self.keep_bytes = keep_bytes
         self._buffers = {}  # the last used at the end
+        self._calls = {}    # of each set, in a list of its own that its outputs hold
         self._bytes = {}    # of each set that may be dropped
         self._used_on = {}  # handles of the streams that may use each set
         self._uncleared = set()
@@ -380,6 +387,7 @@ class Layer:
         new = key not in self._buffers
         if new:
             b = self._make(T, dtype)
+            self._calls[key] = [0]
             self._bytes[key] = sum(t.numel() * t.element_size() for t in b.values()
                                    if t is not None)
             self._used_on[key] = {here}
@@ -404,7 +412,7 @@ class Layer:
             if total <= self.keep_bytes:
                 break
             total -= self._bytes.pop(old)
-            del self._buffers[old], self._used_on[old]
+            del self._buffers[old], self._used_on[old], self._calls[old]
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor,
                 bias: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
@@ -425,14 +433,17 @@ class Layer:
                 return self.forward(x, logits, bias, y)
         T = x.shape[0]
         b = self.buffers(T, x.dtype)
+        calls = self._calls[T, x.dtype]
+        calls[0] += 1
         if y is None:
             y = torch.empty((T, self.d), dtype=x.dtype, device=x.device)
         group_route(self.router, logits, bias, b["idx"], b["w"], b["off"], b["perm"], b["pos"],
                     b["ws"])
         self._experts(b, x)
         combine(b["o"], b["w"], b["pos"], y, shared=b["shared"])
-        return LayerOutput(y=y, **{n: b[n] for n in ("idx", "w", "off", "perm", "pos", "xq", "xs",
-                                                     "hq", "hs", "o", "shared")})
+        return LayerOutput(y=y, call=(calls, calls[0]),
+                           **{n: b[n] for n in ("idx", "w", "off", "perm", "pos", "xq", "xs", "hq",
+                                                "hs", "o", "shared")})
 
     def _experts(self, b: dict, x: torch.Tensor) -> None:
         """The experts' rows b["o"] and the shared expert's b["shared"] of x, once it is routed."""
@@ -449,7 +460,7 @@ class Layer:
     def router_gradients(self, out: LayerOutput, logits: torch.Tensor, dy: torch.Tensor, **kw):
         """What ``dy``, the gradient of ``out.y``, says of the router: see
         ``router_grad.layer_gradients``.  ``out`` is of this layer's last call with as many
-        tokens and the same logits."""
+        tokens (an earlier one's is refused) and the same logits."""
         from . import router_grad
 
         return router_grad.layer_gradients(self.router, out, logits, dy, **kw)

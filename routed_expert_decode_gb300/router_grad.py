@@ -185,7 +185,10 @@ def layer_gradients(router: MoeRouter, out: LayerOutput, logits: torch.Tensor, d
     """The gradient of a layer's router logits [T, E] from ``dy`` [T, d], that of its output
     ``out.y``, and from the balance loss with factor ``coef`` (0: none), which is computed too.
     The experts' weights are taken as constants; ``do`` [R, d], if given, receives the gradient of
-    the experts' output rows.  Runs on the current stream."""
+    the experts' output rows.  ``out`` whose buffers a later call has taken is refused.  Runs on
+    the current stream."""
+    if out.stale:
+        raise ValueError("out is of an earlier call: the layer's buffers hold a later one's values")
     T, k, E = logits.shape[0], router.top_k, router.n_expert
 
     def make(shape, dtype=torch.float32):
