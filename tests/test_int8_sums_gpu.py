@@ -63,6 +63,17 @@ def test_sums_beyond_24_bits(int8, rows, N, K):
     assert rel <= adds * 2 * U32 + U32, rel / U32 / adds
 
 
+@pytest.mark.parametrize("rows,N", [((100,) * 15, 1280), ((2000,), 1040)], ids=["128", "pair"])
+def test_sums_are_cut_off_towards_zero(int8, rows, N):
+    """Sums of the other sign are those of the first, negated, and neither is above the exact
+    one by more than the last rounding."""
+    c = Odd(rows, N, 8208, 3)
+    got, want = c.product(int8), c.exact(70)
+    assert (got[:, -70:].double() <= want * (1 + U32)).all()
+    c.w.neg_()
+    assert torch.equal(c.product(int8), -got)
+
+
 @pytest.mark.parametrize("rows,K", [((1,), 131056), ((3,), 60000), ((40,), 4099),
                                     ((300,), 131071)])
 def test_the_other_kernels_sums_are_exact(int8, rows, K):
