@@ -71,6 +71,15 @@ __device__ __forceinline__ void gr_warm(const GrArgs &a) {
                "l"(a.off), "l"(a.perm), "l"(a.pos), "l"(a.hist), "r"(a.per), "r"(a.per_inv));
 }
 
+// order-preserving map of a float (never NaN) to an unsigned above 0; -0 as +0
+__device__ __forceinline__ uint32_t order_key(float c) {
+  const uint32_t b = __float_as_uint(c + 0.0f);
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+
 __device__ __forceinline__ float load_logit(const void *p, int dt, size_t i) {
   float v;
   if (dt == MOE_DT_F32) v = ((const float *)p)[i];
@@ -85,6 +94,16 @@ __device__ __forceinline__ void stage_token(const void *p, size_t row, uint32_t 
   const typename Elem<DT>::T *src = (const typename Elem<DT>::T *)p + row;
 #pragma unroll 4
   for (uint32_t i = lane; i < E; i += 32) sc[i] = fn(logit_value(Elem<DT>::to(src[i])), i);
+}
+
+// sigmoid and sqrt(softplus) with CUDA's expf and log1pf; -inf gives 0
+__device__ __forceinline__ float sigmoid_of(float l) { return __frcp_rn(1.0f + expf(-l)); }
+__device__ __forceinline__ float softplus_root_of(float l) {
+  return __fsqrt_rn(fmaxf(l, 0.0f) + log1pf(expf(-fabsf(l))));
+}
+// e^(l - max) of a row: 0 at -inf, a row of nothing else included
+__device__ __forceinline__ float softmax_term(float l, float m) {
+  return l == -INFINITY ? 0.0f : expf(l - m);
 }
 
 // One token by one warp: its picks to idx and w.  sc: 32 * NPER floats of shared
