@@ -22,13 +22,13 @@ struct Int8Call {
   uint8_t *ws;
   cudaStream_t stream;
 };
-size_t int8_gemm_ws(uint32_t rows);
+size_t int8_gemm_ws();
 cudaError_t launch_int8_gemm(const Int8Call &c);
 // the same of a few rows in all on CUDA cores (int8_few.cu), same conditions
 cudaError_t launch_int8_few(Fp8Args &a, bool swiglu, cudaStream_t stream);
 // the tensor-core products (int8_tc.cu): operands that tensor copies can take
 bool int8_tc_ok(const Fp8Args &a);
-size_t int8_tc_ws(uint32_t rows);
+size_t int8_tc_ws();
 cudaError_t launch_int8_tc(Fp8Args &a, bool swiglu, cudaStream_t stream);
 
 }  // namespace moe

@@ -27,7 +27,7 @@ moe_status product(const moe_int8_mat *w0, const moe_int8_mat *w1, bool two, uin
   if (x->n == 0 || !x->q || !x->scale || !is_aligned(x->scale, 4)) return MOE_ERR_INVALID_ARG;
   if (!rows_ok(out, odt, ld, x->rows, N)) return MOE_ERR_INVALID_ARG;
   if (!ws || !is_aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < int8_gemm_ws(x->rows)) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < int8_gemm_ws()) return MOE_ERR_WORKSPACE;
   Int8Call c = {};
   c.swiglu = two;
   c.w[0] = *w0;
@@ -60,7 +60,8 @@ moe_status moe_int8_quantize(const void *x, moe_dtype dt, size_t ld, uint32_t T,
   return status_of(launch_int8_quantize(x, dt, ld, T, d, q, scale, (cudaStream_t)stream));
 }
 
-size_t moe_int8_workspace_size(uint32_t rows) { return int8_gemm_ws(rows); }
+// the same for any number of rows: what the shares of split tiles take
+size_t moe_int8_workspace_size(uint32_t) { return int8_gemm_ws(); }
 
 moe_status moe_int8_product(const moe_int8_mat *w, uint32_t n_expert, uint32_t N, uint32_t K,
                             const moe_int8_rows *x, void *out, moe_dtype odt, size_t ld, void *ws,

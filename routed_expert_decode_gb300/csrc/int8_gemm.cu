@@ -119,9 +119,7 @@ bool few_rows(const Fp8Args &a) {
 
 }  // namespace
 
-size_t int8_gemm_ws(uint32_t rows) {
-  return MOE_WS_FIXED_BYTES + int8_tc_ws(rows);
-}
+size_t int8_gemm_ws() { return MOE_WS_FIXED_BYTES + int8_tc_ws(); }
 
 cudaError_t launch_int8_gemm(const Int8Call &c) {
   Fp8Args a = {};

@@ -60,7 +60,7 @@ struct Shape {
   static constexpr int rows = PAIR ? NT / 2 : NT;            // activation rows of a CTA
   static constexpr uint32_t x_bytes = rows * 128;            // ... and their bytes in a stage
   static constexpr int epi = NT >= 128 ? 8 : 4;              // epilogue warps
-  static constexpr int w_sets = NT >= 128 ? 1 : 2;           // sets of weight converters
+  static constexpr int w_sets = NT >= 128 ? 1 : 2;           // sets of weight converters, 1 or 2
   static constexpr int x_warps = NT == 32 ? 2 : rows / 32;   // activation converters of a set
   static constexpr int passes = rows / (x_warps * 4);        // rows of a converting lane
   static constexpr int sets = NT >= 128 ? 2 : (int)ring / 2;  // sets of them
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       bar_init(&w_full[i], 1);
-      bar_init(&w_empty[i], S::w_sets >= 2 ? 8 : 4);
+      bar_init(&w_empty[i], 4 * S::w_sets);
     }
     for (uint32_t i = 0; i < kRing; ++i) {
       bar_init(&full[i], 4 + S::x_warps + (PAIR && !(blockIdx.x & 1)));
@@ -344,28 +344,23 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
   } else if (warp < S::epi0) {
     // ============================ weight converters: half `set` of each stage
     const int set = (warp - 2) >> 2, quarter = warp & 3;
-    constexpr int kHalves = S::w_sets >= 2 ? 2 : 1;       // sets that share a block
-    constexpr int kTurns = S::w_sets / kHalves;           // blocks' sets take turns
     const int row = SWIGLU ? quarter * 16 + (lane & 15) + (lane >> 4) * 64 : quarter * 32 + lane;
     const uint32_t dst = tmem + S::a_column + ((uint32_t)(quarter * 32) << 16);
-    StepRing<kTurns> ws(set / kHalves);
-    StepRing<kTurns> st(set / kHalves);  // of pairs of steps
-    int first = set / kHalves;           // this set's first block of the segment
+    Ring ws, st;  // st: of pairs of steps
     while (!guard.aborted() && walk.take(seg)) {
-      for (int kb = seg.kb0 + first; kb < seg.kb1;
-           kb += kTurns, ws.next(n_w), st.next(S::ring / 2)) {
+      for (int kb = seg.kb0; kb < seg.kb1; ++kb, ws.next(n_w), st.next(S::ring / 2)) {
         bar_wait(&w_full[ws.i], ws.phase, guard);
         // 128-byte swizzle: chunk c of row r at c ^ (r % 8)
         const uint8_t *src = tsm + ws.i * kWBytes + row * 128;
 #pragma unroll
-        for (int h0 = 0; h0 < 2; h0 += kHalves) {
-          const int h = kHalves == 2 ? set & 1 : h0;
+        for (int h0 = 0; h0 < 2; h0 += S::w_sets) {
+          const int h = S::w_sets == 2 ? set : h0;
           const uint32_t stage = 2 * st.i + h;
           uint4 v[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             v[c] = *(const uint4 *)(src + (((h * 4 + c) ^ (row & 7)) << 4));
-          if (h0 + kHalves == 2) {
+          if (h0 + S::w_sets == 2) {
             __syncwarp();
             if (lane == 0) bar_arrive(&w_empty[ws.i]);
           }
@@ -387,7 +382,6 @@ __global__ void __launch_bounds__(Shape<NT, PAIR>::threads, 1)
           if (lane == 0) bar_arrive(&full[stage]);
         }
       }
-      first = (first - (seg.kb1 - seg.kb0) % kTurns + kTurns) % kTurns;
     }
   } else if (warp < S::x0) {
     // ============================ epilogue
@@ -761,10 +755,7 @@ bool int8_tc_ok(const Fp8Args &a) {
 }
 
 // two shares a CTA of a tile of 32 rows
-size_t int8_tc_ws(uint32_t rows) {
-  (void)rows;
-  return (size_t)fp8_ctas() * 2 * 32 * 128 * 4;
-}
+size_t int8_tc_ws() { return (size_t)fp8_ctas() * 2 * 32 * 128 * 4; }
 
 cudaError_t launch_int8_tc(Fp8Args &a, bool swiglu, cudaStream_t stream) {
   return swiglu ? run_planned<true>(a, stream) : run_planned<false>(a, stream);
