@@ -314,12 +314,14 @@ class LayerOutput:
     hs: torch.Tensor
     o: torch.Tensor
     shared: Optional[torch.Tensor]
-    call: Optional[tuple] = None  # the buffers' counter of calls, and what it was at this one
+    # the buffers' counters of calls, which of them counts this one, and what it was then
+    call: Optional[tuple] = None
 
     @property
     def stale(self) -> bool:
-        """Whether a later call of the layer has taken the buffers (a replayed graph is not seen)."""
-        return self.call is not None and self.call[0][0] != self.call[1]
+        """Whether a later call of the layer has taken the buffers.  Calls that a graph captures run
+        when it is replayed, which is not seen: they count among themselves alone."""
+        return self.call is not None and self.call[0][self.call[1]] != self.call[2]
 
 
 class Layer:
@@ -351,7 +353,7 @@ class Layer:
         self.E, self.f, self.d = gate.E, gate.N, gate.K
         self.keep_bytes = keep_bytes
         self._buffers = {}  # the last used at the end
-        self._calls = {}    # of each set, in a list of its own that its outputs hold
+        self._calls = {}    # of each set, plain and captured, in a list that its outputs hold
         self._bytes = {}    # of each set that may be dropped
         self._used_on = {}  # handles of the streams that may use each set
         self._uncleared = set()
@@ -387,7 +389,7 @@ class Layer:
         new = key not in self._buffers
         if new:
             b = self._make(T, dtype)
-            self._calls[key] = [0]
+            self._calls[key] = [0, 0]
             self._bytes[key] = sum(t.numel() * t.element_size() for t in b.values()
                                    if t is not None)
             self._used_on[key] = {here}
@@ -433,15 +435,15 @@ class Layer:
                 return self.forward(x, logits, bias, y)
         T = x.shape[0]
         b = self.buffers(T, x.dtype)
-        calls = self._calls[T, x.dtype]
-        calls[0] += 1
+        calls, kind = self._calls[T, x.dtype], int(_capturing())
+        calls[kind] += 1
         if y is None:
             y = torch.empty((T, self.d), dtype=x.dtype, device=x.device)
         group_route(self.router, logits, bias, b["idx"], b["w"], b["off"], b["perm"], b["pos"],
                     b["ws"])
         self._experts(b, x)
         combine(b["o"], b["w"], b["pos"], y, shared=b["shared"])
-        return LayerOutput(y=y, call=(calls, calls[0]),
+        return LayerOutput(y=y, call=(calls, kind, calls[kind]),
                            **{n: b[n] for n in ("idx", "w", "off", "perm", "pos", "xq", "xs", "hq",
                                                 "hs", "o", "shared")})
 

@@ -50,3 +50,31 @@ def test_outputs_of_a_dropped_set_keep_their_values(int8):  # noqa: F811
     layer.forward(x[:7], logits[:7])   # drops the set of 16
     layer.forward(x.flip(0), logits)   # and makes another
     assert not out.stale and torch.equal(layer.router_gradients(out, logits, dy).dlogits, want)
+
+
+def test_captured_calls_count_apart(int8):  # noqa: F811
+    """A capture runs nothing: an earlier output keeps its values, and a captured one is of its
+    graph's replays, whatever ran between."""
+    rng = np.random.default_rng(4)
+    d, E, T = 128, 8, 24
+    layer = make_layer(int8, rng, E, 2, 1, 1, d, 128, 0)[2]
+    xs = [dev(rng.standard_normal((T, d)).astype(np.float32)).bfloat16() for _ in range(2)]
+    ls = [dev(rng.standard_normal((T, E)).astype(np.float32)) for _ in range(2)]
+    dy = torch.randn((T, d), device="cuda")
+    want = [layer.router_gradients(layer.forward(x, l), l, dy).dlogits for x, l in zip(xs, ls)]
+    plain = layer.forward(xs[0], ls[0])
+    forward, backward = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(forward):
+        first = layer.forward(xs[0], ls[0])
+        captured = layer.forward(xs[1], ls[1])
+    assert first.stale and not plain.stale
+    with pytest.raises(ValueError, match="earlier call"):
+        layer.router_gradients(first, ls[0], dy)
+    assert torch.equal(layer.router_gradients(plain, ls[0], dy).dlogits, want[0])
+    layer.forward(xs[0], ls[0])
+    assert plain.stale and not captured.stale
+    with torch.cuda.graph(backward):
+        g = layer.router_gradients(captured, ls[1], dy)
+    forward.replay()
+    backward.replay()
+    assert torch.equal(g.dlogits, want[1])
