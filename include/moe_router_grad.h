@@ -78,7 +78,7 @@ moe_status moe_route_backward(const moe_router *r, const void *logits, moe_dtype
  * row that several slots name is unspecified; rows that none names are left as they are.
  * o: [R] rows of d values of type dt, stride ldo; dy: [T] rows of type ydt, stride ldy.
  * dw [T][k] or NULL (o is then not read); dout: [R] rows of type dt, stride ldd, or NULL (w
- * is then not read).  dout must not overlap o. */
+ * is then not read).  dout must not overlap o or dy. */
 moe_status moe_combine_backward(const void *dy, moe_dtype ydt, size_t ldy, const void *o,
                                 moe_dtype dt, size_t ldo, uint32_t R, const float *w,
                                 const int32_t *pos, uint32_t T, uint32_t top_k, uint32_t d,

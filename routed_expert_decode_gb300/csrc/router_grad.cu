@@ -11,7 +11,7 @@ namespace {
 
 constexpr int kWarps = 8;
 // CTAs an SM of the logits' gradient by a lane's chunks of experts, all of a grid at a time
-// (65536 x 256 bf16: 33 us, 34 with 4; 32768 x 512: 29, and 37 with a grid of 3)
+// (65536 x 256 bf16: 33 us, 34 with 4, before the tests for tiny scores; 32768 x 512: 29, and 37 with a grid of 3)
 constexpr int back_ctas(int nc) { return nc == 1 ? 3 : nc == 2 ? 2 : 1; }
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kAll = 0xffffffffu;
@@ -597,9 +597,10 @@ __device__ __forceinline__ void store_row(const RouteBackArgs &a, uint32_t t, co
 // coefficients stay in registers from token to token), the picks' part from shared memory.
 // FAST: sigmoid, whole chunks of 8 in and out, the gradient of the logits' type, known when
 // compiling.
-// 65536 x 256 bf16, top 8, with the loss: 33.0 us, of which scores and stores alone are some
-// 20.  35.0 without FAST, and then 37.7 with longer runs for fewer CTAs, 39.1 with the picks
-// token by token, from p laid out in shared memory.  Bound by issue and a token's sums.
+// 65536 x 256 bf16, top 8, with the loss: 34.1 to 34.5 us, of which scores and stores alone are
+// some 20 and the tests for tiny scores 0.5.  Without those 33.0; 35.0 without FAST, and then
+// 37.7 with longer runs for fewer CTAs, 39.1 with the picks token by token, from p laid out in
+// shared memory.  Neither issue (0.57) nor HBM (0.13) is full: a token's sums wait on each other.
 template <int DT, int NC, bool WIDE, bool FAST>
 __global__ void __launch_bounds__(kThreads, back_ctas(NC))
     k_route_backward(const RouteBackArgs a) {

@@ -332,7 +332,8 @@ class Layer:
     triple of one-expert ``Mat`` or None.  Buffers and the workspace are kept per number
     of tokens and type, the last used up to ``keep_bytes`` in all (and those that a
     captured graph uses: its replays need them); calls that overlap need layers (or
-    streams' orders) of their own.  What a call makes, it makes on its stream.
+    streams' orders) of their own.  What a call makes, it makes on its stream.  Nothing is recorded
+    for autograd: the router's gradients are a call of their own (``router_gradients``).
     """
 
     def __init__(self, router: MoeRouter, gate: Mat, up: Mat, down: Mat, shared=None,

@@ -141,7 +141,8 @@ def route_backward(router: MoeRouter, logits, idx, dlogits, dw=None, counts=None
 def combine_backward(dy, o, w, pos, dw=None, do=None, stream=None) -> None:
     """moe_combine_backward: of ``fp8.combine``'s y [T, d], from its gradient ``dy`` [T, d]:
     ``dw`` [T, k] float32, the weights' gradient, and ``do`` [R, d] of o's type, the rows' (each
-    None: not wanted).  ``do`` must not be ``o``; its rows that no slot names stay as they are."""
+    None: not wanted).  ``do`` must not overlap ``o`` or ``dy``; its rows that no slot names stay
+    as they are."""
     dev = dy.get_device()
     if dev < 0 or fp8._many and dev != fp8._current_device():
         return _elsewhere(dev, combine_backward, dy, o, w, pos, dw, do, stream)
