@@ -11,7 +11,8 @@ namespace {
 
 constexpr int kWarps = 8;
 // CTAs an SM of the logits' gradient by a lane's chunks of experts, all of a grid at a time
-// (65536 x 256 bf16: 33 us, 34 with 4, before the tests for tiny scores; 32768 x 512: 29, and 37 with a grid of 3)
+// (before the tests for tiny scores, 65536 x 256 bf16: 33 us, 34 with 4; 32768 x 512: 29, and 37
+// with a grid of 3)
 constexpr int back_ctas(int nc) { return nc == 1 ? 3 : nc == 2 ? 2 : 1; }
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kAll = 0xffffffffu;

@@ -69,7 +69,8 @@ class Small(Batch):
 def levels(T, E, seed):
     """Rows about one level each, from -84 to -111: a constant, a spread of one, and a wide one."""
     g = np.random.default_rng(seed)
-    level = g.choice([-86.0, -87.3, -88.0, -88.6, -88.7, -89.0, -90.0, -95.0, -100.0, -103.0], (T, 1))
+    level = g.choice([-86.0, -87.3, -88.0, -88.6, -88.7, -89.0, -90.0, -95.0, -100.0, -103.0],
+                     (T, 1))
     l = level + g.uniform(-1, 1, (T, E)) * (np.arange(T) % 3 > 0)[:, None]
     wide = np.arange(T) % 3 == 2
     l[wide] = g.uniform(-111, -84, (int(wide.sum()), E))
